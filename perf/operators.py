@@ -253,7 +253,7 @@ def _run_own(s):
     cache = rq.KvCache(s["kc"], s["vc"], s["ks"], s["vs"])
     if c["kind"] == "attend":
         if "ws" not in s:   # a program keeps its workspace
-            n = rq.respin_kv_attention_workspace(cache, c["Hq"], s["N"], c["B"], max_q=s["max_q"])
+            n = rq.respin_kv_attention_workspace(cache, c["Hq"], s["N"], max_q=s["max_q"])
             s["ws"] = torch.empty(n, dtype=torch.uint8, device=DEV)
         rq.respin_kv_attention(cache, s["q"], s["kv_len"], s["table"], s["out"], s["ws"],
                                cu=s["cu"] if s["ragged"] else None, max_q=s["max_q"],
