@@ -239,6 +239,159 @@ respin_status_t respin_quantize_rowmax(const void* u, const float* rowmax,
                                        void* stream);
 
 /*
+ * The attention half of a quantized layer: between the query / key / value
+ * projections (w4a4_gemm) and the quantization of the output projection's
+ * input. bf16 tensors [tokens, heads, head_dim]: heads and head_dim are
+ * contiguous, `ld` is the stride between tokens in elements (a multiple of 8,
+ * at least heads * head_dim), so slices of a projection's output are taken as
+ * they are. head_dim is 64 or 128.
+ */
+
+/*
+ * respin_qk_norm_rope -- norms of queries and keys for each head, and the
+ * position rotation, in one pass. Per token and head vector x, in fp32:
+ *     y = x * w / sqrt(mean(x^2) + eps)     (y = x where the weight is NULL)
+ *     (a, b) -> (a cos t - b sin t, b cos t + a sin t),
+ *     t = positions[n] * inv_freq[i]        (float64, so far positions keep
+ *                                            their angle)
+ * for the pairs (y[i], y[i + rot_dim / 2]) or, interleaved, (y[2i], y[2i+1]),
+ * i < rot_dim / 2; values from rot_dim on are not rotated. One rounding to
+ * bf16 at the end.
+ *
+ *   q, k       : bf16 [N, q_heads | kv_heads, head_dim]; either may have 0
+ *                heads (its pointers are then unused).
+ *   N          : tokens; 0 is a no-op.
+ *   q_weight   : bf16 [head_dim] or NULL (no norm of queries); k_weight same.
+ *   eps        : 1e-20 <= eps < 1e20 (only looked at with a weight).
+ *   positions  : int32 [N]; inv_freq: fp32 [rot_dim / 2] (both device; unused
+ *                for rot_dim 0).
+ *   rot_dim    : 0 .. head_dim, a multiple of 16.
+ *   q_out      : bf16, may be q itself with the same stride (k_out same); no
+ *                other overlap.
+ * Pointers 16-byte aligned (positions, inv_freq 4). Errors: INVALID_ARG,
+ * UNSUPPORTED, ALIGNMENT, CUDA.
+ */
+respin_status_t respin_qk_norm_rope(const void* q, const void* k, int N,
+                                    int q_heads, int kv_heads, int head_dim,
+                                    long long ld_q, long long ld_k,
+                                    const void* q_weight, const void* k_weight,
+                                    float eps, const int32_t* positions,
+                                    const float* inv_freq, int rot_dim,
+                                    int interleaved, void* q_out, void* k_out,
+                                    long long ld_qo, long long ld_ko,
+                                    void* stream);
+
+/*
+ * The 8-bit key/value cache: pages of page_size tokens, one fp32 scale for
+ * each page and head; a code c stands for c * scale. Memory is the caller's
+ * (device); a page's contents mean nothing until respin_kv_append wrote it.
+ */
+typedef struct {
+  int8_t* k;       /* [num_pages, kv_heads, page_size, head_dim], 16-byte aligned */
+  int8_t* v;
+  float* k_scale;  /* [num_pages, kv_heads] */
+  float* v_scale;
+  int num_pages;   /* num_pages * kv_heads * page_size < 2^31 */
+  int page_size;   /* 16, 32, 64 or 128 */
+  int kv_heads;    /* 1 .. 1024 */
+  int head_dim;    /* 64 or 128 */
+} respin_kv_cache_t;
+
+/*
+ * A ragged batch: the last tokens of B sequences, packed. Rows cu[b] ..
+ * cu[b+1] - 1 of the call's tensors are the last cu[b+1] - cu[b] tokens of
+ * sequence b; kv_len[b] is its length WITH them, so row cu[b] + i has
+ * position kv_len[b] - (cu[b+1] - cu[b]) + i. Token t of a sequence is slot
+ * t % page_size of page block_table[b][t / page_size]; entries behind the
+ * last used page are not read. Rows from cu[B] on are left as they are.
+ *
+ * The arrays are device memory and are checked on the device: a cu or kv_len
+ * that does not fit (negative, decreasing, beyond N or the table) or a page id
+ * outside the cache is recorded (respin_device_status: 512, 511) and its
+ * tokens are left out; nothing outside the given buffers is touched.
+ */
+typedef struct {
+  const int32_t* cu;           /* [B + 1], or NULL: N / B rows each */
+  const int32_t* kv_len;       /* [B] */
+  const int32_t* block_table;  /* [B, max_pages] */
+  int B;                       /* 0 .. 65536 */
+  int max_pages;
+  int N;                       /* rows; 0 is a no-op */
+} respin_kv_batch_t;
+
+/*
+ * respin_kv_append -- quantize new keys and values into the cache. Per page
+ * and head, in binary32 (round to nearest even), over the call's new values x
+ * of that page (finite ones for the maximum):
+ *     a = max |x|,  s = max(s_old, a / 127),  s < 2^-126 becomes 0
+ *     earlier codes c of the page -> rint(c * (s_old / s))
+ *     q = clamp(rint(x * (1 / s)), -127, 127)      (0 where s is 0)
+ * s_old is the page's scale if it holds earlier tokens of the sequence, else
+ * 0. Infinities are stored as +-127 and NaN as 0, so the cache stays finite.
+ * Slots that hold no token of the sequence keep their bytes. Appending the
+ * same tokens at the same place again changes nothing.
+ *
+ *   k, v : bf16 [N, kv_heads, head_dim] (strides ld_k, ld_v).
+ * A page that takes new tokens must belong to one sequence of the call (pages
+ * that are only read may be shared). Errors: INVALID_ARG, UNSUPPORTED,
+ * ALIGNMENT, CUDA.
+ */
+respin_status_t respin_kv_append(const respin_kv_cache_t* cache,
+                                 const respin_kv_batch_t* batch, const void* k,
+                                 const void* v, long long ld_k, long long ld_v,
+                                 void* stream);
+
+/* respin_kv_read -- read tokens of the cache back: row n of k_out and v_out
+ * (bf16 [N, kv_heads, head_dim]) is bf16(code * scale) of the batch's row n.
+ * Errors: as respin_kv_append. */
+respin_status_t respin_kv_read(const respin_kv_cache_t* cache,
+                               const respin_kv_batch_t* batch, void* k_out,
+                               void* v_out, long long ld_k, long long ld_v,
+                               void* stream);
+
+/*
+ * respin_kv_attention -- attention of the batch's rows over the cache, which
+ * already holds their own keys and values. Query head h reads key head
+ * h / (q_heads / kv_heads). For a row at position p of a sequence of length n:
+ *     s_j = scale * (q . k_j),  j < n
+ *           and j <= p (causal)  and j > p - window (window > 0)
+ *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
+ * A row that sees no token gets out 0 and lse -inf. Products are exact and
+ * sums fp32; the weights are rounded to fp16 before the second product and
+ * the output to bf16.
+ *
+ *   q         : bf16 [N, q_heads, head_dim] (stride ld_q).
+ *   q_heads   : a multiple of kv_heads, at most 1024.
+ *   max_q     : at least the most rows of a sequence, 0 if unknown.
+ *   causal    : 0 or 1; window: 0 (none) or the last tokens a row sees, its
+ *               own among them (needs causal).
+ *   out       : bf16 [N, q_heads, head_dim] (stride ld_out).
+ *   lse       : fp32 [N, q_heads] or NULL.
+ *   workspace : device, 16-byte aligned, of the size that
+ *               respin_kv_attention_workspace gives; needs no set-up and holds
+ *               nothing between calls. Calls that may run at the same time
+ *               (other streams, graphs that may overlap) need one each.
+ * The sums' order depends on the batch's lengths and the device, not on
+ * timing: a repeated call gives the same bits. Errors: INVALID_ARG,
+ * UNSUPPORTED, ALIGNMENT, CUDA.
+ */
+respin_status_t respin_kv_attention(const respin_kv_cache_t* cache,
+                                    const respin_kv_batch_t* batch,
+                                    const void* q, int q_heads, long long ld_q,
+                                    int max_q, int causal, int window,
+                                    float scale, void* out, long long ld_out,
+                                    float* lse, void* workspace,
+                                    long long workspace_bytes, void* stream);
+
+/* respin_kv_attention_workspace -- bytes of the workspace of a call with N
+ * rows, at most max_q (0: unknown) of a sequence. Host only; does not grow
+ * with the contexts or the number of sequences. Errors: INVALID_ARG,
+ * UNSUPPORTED. */
+respin_status_t respin_kv_attention_workspace(int q_heads, int kv_heads,
+                                              int head_dim, int N, int max_q,
+                                              long long* bytes);
+
+/*
  * respin_factors_from_subspace -- plan factors from the subspace form.
  *
  * Passage: zh §2.2 steps 1-3 store one D x r basis Q and an r x r rotation
@@ -327,7 +480,8 @@ respin_status_t respin_quantize_weight(int O, int K, const float* W, int qmax,
 
 /* respin_device_status -- synchronizes the current device, then returns and
  * clears the device status word through *code (0 = no kernel gave up; else
- * the site of the first wait that gave up since the last clear). Returns
+ * the site of the first wait that gave up, or 511 / 512 for the first index
+ * of a cache call that was refused, since the last clear). Returns
  * DEVICE_CHECK if *code != 0. The outputs of a launch in which a wait gave up
  * are invalid (the kernel skips its stores after the failure); the status
  * word itself never changes what a later launch computes. */

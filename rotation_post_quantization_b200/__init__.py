@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -29,10 +30,25 @@ RESPIN_ACT_INT3 = 2
 EXPORTED = ("respin_plan_create", "respin_plan_create_subspace", "respin_plan_destroy",
             "respin_boundary_forward", "w4a4_gemm", "w4a4_gemm_i32",
             "w4a4_gemm_rowmax", "respin_quantize_rowmax",
+            "respin_qk_norm_rope", "respin_kv_append", "respin_kv_read",
+            "respin_kv_attention", "respin_kv_attention_workspace",
             "respin_factors_from_subspace", "respin_factors_from_transition",
             "respin_fuse_weight", "respin_quantize_weight",
             "respin_device_status", "respin_selftest_wait_limit",
             "respin_last_error", "respin_version")
+
+
+class _KvCacheC(ctypes.Structure):
+    """respin_kv_cache_t"""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class _KvBatchC(ctypes.Structure):
+    """respin_kv_batch_t"""
+    _fields_ = [("cu", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("B", ctypes.c_int), ("max_pages", ctypes.c_int), ("N", ctypes.c_int)]
 
 
 class RespinError(RuntimeError):
@@ -60,6 +76,14 @@ def _load() -> ctypes.CDLL:
     lib.w4a4_gemm_i32.argtypes = [vp, vp, i32, i32, i32, vp, vp]
     lib.w4a4_gemm_rowmax.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp]
     lib.respin_quantize_rowmax.argtypes = [vp, vp, i32, i32, vp, vp, u32, vp]
+    i64, f32 = ctypes.c_longlong, ctypes.c_float
+    cp, bp = ctypes.POINTER(_KvCacheC), ctypes.POINTER(_KvBatchC)
+    lib.respin_qk_norm_rope.argtypes = [vp, vp, i32, i32, i32, i32, i64, i64, vp, vp, f32, vp, vp, i32, i32,
+                                        vp, vp, i64, i64, vp]
+    lib.respin_kv_append.argtypes = [cp, bp, vp, vp, i64, i64, vp]
+    lib.respin_kv_read.argtypes = [cp, bp, vp, vp, i64, i64, vp]
+    lib.respin_kv_attention.argtypes = [cp, bp, vp, i32, i64, i32, i32, i32, f32, vp, i64, vp, vp, i64, vp]
+    lib.respin_kv_attention_workspace.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(i64)]
     dp = ctypes.POINTER(ctypes.c_double)
     lib.respin_factors_from_subspace.argtypes = [i32, i32, fp, fp, fp, fp]
     lib.respin_factors_from_transition.argtypes = [i32, i32, fp, ctypes.c_double, fp, fp, dp]
@@ -211,6 +235,167 @@ def respin_quantize_rowmax(u, rowmax, q_packed, scale, flags: int = 0, stream=No
     N, D = u.shape
     _check(lib.respin_quantize_rowmax(_ptr(u), _ptr(rowmax), int(N), int(D), _ptr(q_packed),
                                       _ptr(scale), ctypes.c_uint(flags), _stream(stream)))
+
+
+def _want(t, name, dtype, shape, like=None):
+    """Check a tensor's type, shape (None: any size) and device; the kernels
+    read what these say is there."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    s = t.shape
+    if len(s) != len(shape) or any(w is not None and w != g for w, g in zip(shape, s)):
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(s)}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _heads_ld(t, name):
+    """Stride between tokens of [N, heads, head_dim] with contiguous heads."""
+    st, s = t.stride(), t.shape
+    if st[2] != 1 and s[2] > 1 or st[1] != s[2] and s[1] > 1:
+        raise ValueError(f"{name}: heads and head_dim must be contiguous (strides {list(st)})")
+    return st[0] if s[0] > 1 else max(8, s[1] * s[2])
+
+
+def _current_device(t, name):
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+
+
+class KvCache(NamedTuple):
+    """The 8-bit paged key/value cache: codes int8 [num_pages, kv_heads,
+    page_size, head_dim] and scales fp32 [num_pages, kv_heads]; a code c of a
+    page and head stands for c * scale."""
+    k: "torch.Tensor"
+    v: "torch.Tensor"
+    k_scale: "torch.Tensor"
+    v_scale: "torch.Tensor"
+
+    @classmethod
+    def empty(cls, num_pages: int, page_size: int, kv_heads: int, head_dim: int, device="cuda") -> "KvCache":
+        import torch
+        shape = (num_pages, kv_heads, page_size, head_dim)
+        return cls(torch.zeros(shape, dtype=torch.int8, device=device), torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+
+def _kv_args(cache, N, kv_len, block_table, cu):
+    """(respin_kv_cache_t, respin_kv_batch_t) of checked tensors."""
+    import torch
+    k, v, ks, vs = cache
+    _current_device(k, "cache.k")
+    _want(k, "cache.k", torch.int8, (None,) * 4)
+    pages, heads, page_size, d = k.shape
+    _want(v, "cache.v", torch.int8, k.shape, k)
+    _want(ks, "cache.k_scale", torch.float32, (pages, heads), k)
+    _want(vs, "cache.v_scale", torch.float32, (pages, heads), k)
+    B = kv_len.shape[0]
+    _want(kv_len, "kv_len", torch.int32, (B,), k)
+    _want(block_table, "block_table", torch.int32, (B, None), k)
+    if cu is not None:
+        _want(cu, "cu", torch.int32, (B + 1,), k)
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and kv_len.is_contiguous() and block_table.is_contiguous() and (cu is None or cu.is_contiguous())):
+        raise ValueError("the cache, kv_len, block_table and cu must be contiguous")
+    return (_KvCacheC(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page_size, heads, d),
+            _KvBatchC(None if cu is None else cu.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+                      B, block_table.shape[1], N))
+
+
+def respin_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """Per-head RMS norm (where a weight is given) and position rotation of
+    q [N, q_heads, d] and k [N, kv_heads, d] (bf16, any token stride) into
+    q_out and k_out (which may be q and k). positions: int32 [N]; inv_freq:
+    fp32 [rot_dim / 2]."""
+    import torch
+    bf = torch.bfloat16
+    _current_device(q, "q")
+    _want(q, "q", bf, (None, None, None))
+    N, Hq, d = q.shape
+    _want(k, "k", bf, (N, None, d), q)
+    Hk = k.shape[1]
+    _want(q_out, "q_out", bf, q.shape, q)
+    _want(k_out, "k_out", bf, k.shape, q)
+    _want(positions, "positions", torch.int32, (N,), q)
+    _want(inv_freq, "inv_freq", torch.float32, (None,), q)
+    if not (positions.is_contiguous() and inv_freq.is_contiguous()):
+        raise ValueError("positions and inv_freq must be contiguous")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _want(w, name, bf, (d,), q)
+            if not w.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    _check(lib.respin_qk_norm_rope(
+        q.data_ptr(), k.data_ptr(), N, Hq, Hk, d, _heads_ld(q, "q"), _heads_ld(k, "k"), _ptr(q_weight),
+        _ptr(k_weight), eps, positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved),
+        q_out.data_ptr(), k_out.data_ptr(), _heads_ld(q_out, "q_out"), _heads_ld(k_out, "k_out"), _stream(stream)))
+
+
+def respin_kv_append(cache: KvCache, k, v, kv_len, block_table, cu=None, stream=None) -> None:
+    """Quantize the new keys and values k, v (bf16 [N, kv_heads, d], any token
+    stride) into the cache. They are the last tokens of B sequences: kv_len
+    int32 [B] counts them already, cu int32 [B + 1] says whose rows are whose
+    (None: N / B each), block_table int32 [B, max_pages] names the pages."""
+    import torch
+    N = k.shape[0]
+    c, b = _kv_args(cache, N, kv_len, block_table, cu)
+    shape = (N, c.kv_heads, c.head_dim)
+    _want(k, "k", torch.bfloat16, shape, cache.k)
+    _want(v, "v", torch.bfloat16, shape, cache.k)
+    _check(lib.respin_kv_append(c, b, k.data_ptr(), v.data_ptr(), _heads_ld(k, "k"), _heads_ld(v, "v"), _stream(stream)))
+
+
+def respin_kv_read(cache: KvCache, k_out, v_out, kv_len, block_table, cu=None, stream=None) -> None:
+    """Read the last tokens of B sequences back into k_out, v_out (bf16
+    [N, kv_heads, d]); kv_len, block_table and cu as in respin_kv_append."""
+    import torch
+    N = k_out.shape[0]
+    c, b = _kv_args(cache, N, kv_len, block_table, cu)
+    shape = (N, c.kv_heads, c.head_dim)
+    _want(k_out, "k_out", torch.bfloat16, shape, cache.k)
+    _want(v_out, "v_out", torch.bfloat16, shape, cache.k)
+    _check(lib.respin_kv_read(c, b, k_out.data_ptr(), v_out.data_ptr(), _heads_ld(k_out, "k_out"),
+                              _heads_ld(v_out, "v_out"), _stream(stream)))
+
+
+def respin_kv_attention_workspace(cache: KvCache, q_heads: int, N: int, max_q=None) -> int:
+    """Bytes of the workspace of respin_kv_attention for N query rows, at most
+    max_q of a sequence (None: unknown, enough for any)."""
+    n = ctypes.c_longlong(0)
+    _check(lib.respin_kv_attention_workspace(q_heads, cache.k.shape[1], cache.k.shape[3], N, max_q or 0, ctypes.byref(n)))
+    return n.value
+
+
+def respin_kv_attention(cache: KvCache, q, kv_len, block_table, out, workspace, cu=None, max_q=None,
+                        causal: bool = True, window: int = 0, scale=None, lse=None, stream=None) -> None:
+    """Attention of q (bf16 [N, q_heads, d]: the last tokens of B sequences,
+    already appended) over the cache into out (bf16, q's shape) and lse (fp32
+    [N, q_heads], optional). max_q: at least the most rows of a sequence (None:
+    N / B without cu, N with). scale: d ** -0.5 by default. workspace: uint8,
+    respin_kv_attention_workspace bytes, one for each call that may run at the
+    same time. kv_len, block_table and cu as in respin_kv_append."""
+    import torch
+    N = q.shape[0]
+    c, b = _kv_args(cache, N, kv_len, block_table, cu)
+    k, d = cache.k, c.head_dim
+    _want(q, "q", torch.bfloat16, (N, None, d), k)
+    Hq = q.shape[1]
+    _want(out, "out", torch.bfloat16, (N, Hq, d), k)
+    _want(workspace, "workspace", torch.uint8, (None,), k)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (N, Hq), k)
+        if not lse.is_contiguous():
+            raise ValueError("lse must be contiguous")
+    if cu is None and b.B > 0:
+        max_q = N // b.B
+    _check(lib.respin_kv_attention(c, b, q.data_ptr(), Hq, _heads_ld(q, "q"), max_q or 0, int(causal), int(window),
+                                   d ** -0.5 if scale is None else scale, out.data_ptr(), _heads_ld(out, "out"),
+                                   _ptr(lse), workspace.data_ptr(), workspace.shape[0], _stream(stream)))
 
 
 def _host_f32(a, shape, name):

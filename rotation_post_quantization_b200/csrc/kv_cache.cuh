@@ -1,0 +1,294 @@
+// The 8-bit key/value cache: pages of int8 codes with one fp32 scale for each
+// page and head, written (quantized) and read back.
+//
+//   codes [pages][heads][P][D] int8, scales [pages][heads] fp32,
+//   value = code * scale;  token t of sequence b is slot t % P of page
+//   table[b][t / P].
+//
+// Writing. With a = max |x| over the finite new values of a page and head
+// (binary32, every operation rounded to nearest even):
+//   s = max(s_old, a / 127)     s_old: the page's scale if it holds earlier
+//                               tokens of the sequence, else 0
+//   s < 2^-126 -> 0
+//   earlier codes c -> rint(c * (s_old / s)), left alone while s = s_old
+//   new codes = clamp(rint(x * (1 / s)), -127, 127); NaN -> 0; all 0 for s = 0
+// A page of a call's tokens belongs to one block per head and tensor, which
+// sees all of them, so nothing depends on an order of blocks and a repeated
+// call finds s = s_old and writes the same bytes again.
+//
+// Both directions are memory bound (3 bytes an element).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace respin {
+
+// Device view of a cache and of a ragged batch of the last tokens of its
+// sequences: rows cu[b] .. cu[b + 1] - 1 are the last ones of sequence b,
+// whose length with them is kv_len[b]. cu == nullptr: `per` rows each.
+struct KvView {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int pages, P, H;
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int B, max_pages, N, per;
+};
+
+// Rows of sequence b: [begin, end) within [0, N), or an empty range, and its
+// length. What does not fit the batch or the block table is recorded and
+// taken as empty.
+__device__ __forceinline__ bool kv_rows(const KvView& c, int b, int& begin, int& end, int& len) {
+  begin = c.cu ? c.cu[b] : b * c.per;
+  end = c.cu ? c.cu[b + 1] : begin + c.per;
+  len = c.kv_len[b];
+  const bool ok = begin >= 0 && begin <= end && end <= c.N && len >= 0 &&
+                  static_cast<long long>(len) <= static_cast<long long>(c.max_pages) * c.P;
+  if (!ok) {
+    record_status(kSiteKvLength);
+    begin = end = 0;
+    len = 0;
+  }
+  return ok;
+}
+
+// Sequence of row r, or B when no sequence holds it (rows behind the last
+// one). Every lane of the warp calls it with the same r: 32 sequences are
+// looked at in a step, so 32 take one and 1024 two round trips to memory.
+__device__ __forceinline__ int kv_find(const KvView& c, int r) {
+  if (c.cu == nullptr) return r / c.per;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = c.B;   // the first b with cu[b + 1] > r lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < hi && c.cu[at + 1] <= r;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, below));
+    if (n == 0) break;
+    const int first = lo + (n - 1) * step + 1;
+    hi = min(hi, lo + n * step);
+    lo = first;
+  }
+  return lo;
+}
+
+// Page id of token t of sequence b, or -1 (recorded) outside the cache.
+__device__ __forceinline__ int kv_page(const KvView& c, int b, int t) {
+  const int id = c.table[static_cast<long long>(b) * c.max_pages + t / c.P];
+  if (id >= 0 && id < c.pages) return id;
+  record_status(kSiteKvPage);
+  return -1;
+}
+
+constexpr int kKvScaleChunks = 8;   // 16-byte pieces of new values a thread holds
+
+struct KvAppendArgs {
+  KvView c;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long ldk, ldv;   // elements between tokens
+  int rows;             // rows of a block
+};
+
+// max |x| of eight bf16 values, finite ones only, as the bits of a bf16.
+__device__ __forceinline__ uint32_t bf16x8_finite_amax(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+    m = max(m, lo < 0x7F80u ? lo : 0u);
+    m = max(m, hi < 0x7F80u ? hi : 0u);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint32_t kv_code(float x, float inv) {
+  const int q = __float2int_rn(__fmul_rn(x, inv));   // NaN -> 0, saturates
+  return static_cast<uint32_t>(max(-127, min(127, q))) & 0xFFu;
+}
+
+// grid (row chunks, heads, K | V). The block's rows are cut at page
+// boundaries and sequence ends; it owns the pages whose first new token is
+// one of its rows. T threads hold a page's new values in registers
+// (P * D / 8 <= kKvScaleChunks * T), so the second look at them is free.
+template <int D, int T>
+__global__ void __launch_bounds__(T) kv_append_kernel(const KvAppendArgs a) {
+  constexpr int L = D / 8;   // 16-byte pieces of a token
+  __shared__ uint32_t amax_warp[T / 32];
+  const KvView& c = a.c;
+  const int tid = threadIdx.x, h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const __nv_bfloat16* src = (is_v ? a.v : a.k) + static_cast<long long>(h) * D;
+  const long long ld = is_v ? a.ldv : a.ldk;
+  int8_t* const codes0 = is_v ? c.v : c.k;
+  float* const scales0 = is_v ? c.v_scale : c.k_scale;
+
+  grid_dep_wait();
+  grid_dep_launch();
+  int r = blockIdx.x * a.rows;
+  const int stop = min(c.N, r + a.rows);
+  while (r < stop) {
+    const int b = kv_find(c, r);
+    if (b >= c.B) break;
+    int begin, end, len;
+    if (!kv_rows(c, b, begin, end, len) || r < begin || r >= end) {
+      ++r;   // (an unordered cu: nothing to rely on)
+      continue;
+    }
+    const int start = len - (end - begin);          // position of the first new token
+    if (start < 0) {                                // more new tokens than the sequence has
+      record_status(kSiteKvLength);
+      r = end;
+      continue;
+    }
+    const int pos = start + (r - begin);
+    const int slot = pos % c.P;
+    const int n = min(end - r, c.P - slot);         // new tokens of this page from here on
+    if (r != begin && slot != 0) {                  // another block owns this page
+      r += n;
+      continue;
+    }
+    const int page = kv_page(c, b, pos);
+    if (page >= 0) {
+      int8_t* codes = codes0 + (static_cast<long long>(page) * c.H + h) * c.P * D;
+      float* scale = scales0 + static_cast<long long>(page) * c.H + h;
+      const float s_old = slot > 0 ? *scale : 0.0f;
+      const int pieces = n * L;
+      uint4 buf[kKvScaleChunks];
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < kKvScaleChunks; ++i) {
+        const int p = tid + i * T;
+        buf[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p < pieces) buf[i] = reinterpret_cast<const uint4*>(src + (r + p / L) * ld)[p % L];
+      }
+#pragma unroll
+      for (int i = 0; i < kKvScaleChunks; ++i) m = max(m, bf16x8_finite_amax(buf[i]));
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if ((tid & 31) == 0) amax_warp[tid / 32] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < T / 32; ++w) m = max(m, amax_warp[w]);
+      float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
+      if (s < 1.17549435e-38f) s = 0.0f;
+      const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+      const float ratio = s > 0.0f ? __fdiv_rn(s_old, s) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kKvScaleChunks; ++i) {
+        const int p = tid + i * T;
+        if (p < pieces) {
+          float x[8];
+          uint32_t q[8];
+          bf16x8_to_f32(buf[i], x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = s > 0.0f ? kv_code(x[j], inv) : 0u;
+          const uint2 w = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
+                                     q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+          reinterpret_cast<uint2*>(codes + (slot + p / L) * D)[p % L] = w;
+        }
+      }
+      if (slot > 0 && ratio != 1.0f) {   // the page's earlier tokens take the larger scale
+        for (int p = tid; p < slot * (D / 4); p += T) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(codes) + p;
+          const uint32_t w = *at;
+          uint32_t o = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o |= kv_code(static_cast<float>(static_cast<int8_t>(w >> (8 * j))), ratio) << (8 * j);
+          *at = o;
+        }
+      }
+      __syncthreads();   // every thread has read the old scale and the maxima
+      if (tid == 0) *scale = s;
+    }
+    r += n;
+  }
+}
+
+struct KvReadArgs {
+  KvView c;
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  long long ldk, ldv;
+};
+
+constexpr int kKvReadRows = 16;
+constexpr int kKvReadThreads = 128;
+
+// grid (chunks of 16 rows, K | V). The rows' pages are found first; then the
+// block walks heads, rows and 16-byte pieces of codes: neighbouring rows of a
+// page are neighbours in memory, so a head's 16 rows are one run of codes.
+template <int D>
+__global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArgs a) {
+  constexpr int L = D / 16;   // 16-byte pieces of a token's codes
+  __shared__ int page_of[kKvReadRows], slot_of[kKvReadRows];
+  const KvView& c = a.c;
+  const int tid = threadIdx.x, warp = tid / 32;
+  const bool is_v = blockIdx.y != 0;
+  const int8_t* const codes = is_v ? c.v : c.k;
+  const float* const scales = is_v ? c.v_scale : c.k_scale;
+  __nv_bfloat16* const out = is_v ? a.v : a.k;
+  const long long ld = is_v ? a.ldv : a.ldk;
+  const int r0 = blockIdx.x * kKvReadRows;
+
+  grid_dep_wait();
+  grid_dep_launch();
+  int begin = 0, end = 0, len = 0, b = 0;
+  constexpr int kPerWarp = kKvReadRows / (kKvReadThreads / 32);
+  for (int i = 0; i < kPerWarp; ++i) {
+    const int r = r0 + warp * kPerWarp + i;
+    int page = -1, slot = 0;
+    if (r < c.N) {
+      if (r < begin || r >= end) {
+        b = kv_find(c, r);
+        if (b >= c.B || !kv_rows(c, b, begin, end, len)) begin = end = 0;
+      }
+      if (r >= begin && r < end) {
+        const int pos = len - (end - r);
+        if (pos >= 0) {
+          page = kv_page(c, b, pos);
+          slot = pos % c.P;
+        } else {
+          record_status(kSiteKvLength);
+        }
+      }
+    }
+    if ((tid & 31) == 0) {
+      page_of[warp * kPerWarp + i] = page;
+      slot_of[warp * kPerWarp + i] = slot;
+    }
+  }
+  __syncthreads();
+  const int total = c.H * kKvReadRows * L;
+#pragma unroll 4
+  for (int p = tid; p < total; p += kKvReadThreads) {
+    const int piece = p % L, row = (p / L) % kKvReadRows, h = p / (L * kKvReadRows);
+    const int page = page_of[row];
+    if (page < 0) continue;
+    const long long ph = static_cast<long long>(page) * c.H + h;
+    const uint4 w = reinterpret_cast<const uint4*>(codes + (ph * c.P + slot_of[row]) * D)[piece];
+    const float s = scales[ph];
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(in[i] >> (8 * j))), s);
+      o[2 * i] = pack_bf16x2(x[0], x[1]);
+      o[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+    }
+    uint4* to = reinterpret_cast<uint4*>(out + (r0 + row) * ld + static_cast<long long>(h) * D) + 2 * piece;
+    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+}  // namespace respin

@@ -28,6 +28,11 @@ enum StatusSite : int {
   kSiteTcLoad = 401,         // tensor-core boundary passes: waiting for a staged tile
   kSiteTcFree = 402,         // tensor-core boundary passes: waiting for a free stage
   kSiteTcAccum = 403,        // tensor-core boundary passes: waiting for accumulators / operand A
+  kSiteKvLoad = 501,         // attention: waiting for a staged tile of the cache
+  kSiteKvFree = 502,         // attention: waiting for a free stage
+  kSiteKvAccum = 503,        // attention: waiting for scores, weights or accumulators
+  kSiteKvPage = 511,         // cache calls: a page id outside the cache (its tokens are left out)
+  kSiteKvLength = 512,       // cache calls: cu or kv_len outside the batch or the block table
   kSiteSelfTest = 901,       // respin_selftest_wait_limit: a wait that nothing completes
 };
 
@@ -385,6 +390,15 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 
 // ---------------------------------------------------------------- tcgen05

@@ -24,6 +24,9 @@
 #include "boundary_rowtile.cuh"
 #include "boundary_tc.cuh"
 #include "factor_builder.h"
+#include "kv_attention.cuh"
+#include "kv_cache.cuh"
+#include "qk_norm_rope.cuh"
 #include "weight_tool.h"
 #include "w4a4_gemm_kernels.cuh"
 #include "w4a4_gemm_skinny.cuh"
@@ -1261,3 +1264,5 @@ respin_status_t respin_device_status(int* code) {
 }
 
 }  // extern "C"
+
+#include "kv_api.cuh"
