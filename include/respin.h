@@ -362,7 +362,8 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache,
  *
  *   q         : bf16 [N, q_heads, head_dim] (stride ld_q).
  *   q_heads   : a multiple of kv_heads, at most 1024.
- *   max_q     : at least the most rows of a sequence, 0 if unknown.
+ *   max_q     : at least the most rows of a sequence, 0 if unknown (a value
+ *               below the truth may leave longer sequences out: 512).
  *   causal    : 0 or 1; window: 0 (none) or the last tokens a row sees, its
  *               own among them (needs causal).
  *   out       : bf16 [N, q_heads, head_dim] (stride ld_out).

@@ -62,34 +62,46 @@ cudaError_t launch_dependent3(const void* fn, dim3 grid, int block, size_t smem,
 
 struct KvAttnVariant {
   const void* fn;
-  const void* combine;
   size_t smem;
-  int rows;         // of a group
-  long long slot;   // floats of a partial result
+  int threads;
+  int rows;            // of a partial result
+  long long slot;      // floats of one
 };
 
 template <int D, int NT>
-KvAttnVariant kv_variant() {
+KvAttnVariant kv_few() {
   using C = KvAttnCfg<D, NT>;
-  return {reinterpret_cast<const void*>(&kv_attn_kernel<D, NT>), reinterpret_cast<const void*>(&kv_combine_kernel<D, C::RB>),
-          static_cast<size_t>(C::Smem), C::RB, static_cast<long long>(C::SlotFloats)};
+  return {reinterpret_cast<const void*>(&kv_attn_kernel<D, NT>), static_cast<size_t>(C::Smem), kKvThreads, C::RB,
+          static_cast<long long>(C::SlotFloats)};
 }
 
-// At most 8 rows a key head (single tokens): one n = 8 product, else two.
-KvAttnVariant kv_pick(int D, long long rows) {
-  if (D == 64) return rows <= 8 ? kv_variant<64, 1>() : kv_variant<64, 2>();
-  return rows <= 8 ? kv_variant<128, 1>() : kv_variant<128, 2>();
+template <int D>
+KvAttnVariant kv_many() {
+  using C = TcaCfg<D>;
+  return {reinterpret_cast<const void*>(&kv_attn_tc_kernel<D>), static_cast<size_t>(C::Smem), kTcaThreads, kTcaGroup,
+          static_cast<long long>(C::SlotFloats)};
 }
 
-constexpr int kKvVariants = 4;
+constexpr int kKvVariants = 6;
+
+// Variants 0, 1: at most 8 rows a key head (single tokens: one n = 8 product)
+// or kKvFewRows; 2: more (tensor memory). Then the same for head_dim 128.
+KvAttnVariant kv_variant(int i) {
+  switch (i) {
+    case 0: return kv_few<64, 1>();
+    case 1: return kv_few<64, 2>();
+    case 2: return kv_many<64>();
+    case 3: return kv_few<128, 1>();
+    case 4: return kv_few<128, 2>();
+    default: return kv_many<128>();
+  }
+}
 
 struct KvDeviceInfo {
   bool ready = false;
   int sms = 0;
-  int occ[kKvVariants] = {0, 0, 0, 0};   // resident blocks per SM
+  int occ[kKvVariants] = {0, 0, 0, 0, 0, 0};   // resident blocks per SM
 };
-
-int kv_variant_index(int D, int rows) { return (D == 128 ? 2 : 0) + (rows > 8 ? 1 : 0); }
 
 cudaError_t kv_prepare(int dev, KvDeviceInfo* info) {
   static std::mutex mu;
@@ -99,13 +111,12 @@ cudaError_t kv_prepare(int dev, KvDeviceInfo* info) {
   KvDeviceInfo& d = infos[dev];
   if (!d.ready) {
     cudaError_t e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    for (int D = 64; D <= 128 && e == cudaSuccess; D += 64)
-      for (int rows = 8; rows <= 16 && e == cudaSuccess; rows += 8) {
-        const KvAttnVariant v = kv_pick(D, rows);
-        e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem));
-        if (e == cudaSuccess)
-          e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.occ[kv_variant_index(D, rows)], v.fn, kKvThreads, v.smem);
-      }
+    for (int i = 0; i < kKvVariants && e == cudaSuccess; ++i) {
+      const KvAttnVariant v = kv_variant(i);
+      e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(v.smem));
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&d.occ[i], v.fn, v.threads, v.smem);
+      if (e == cudaSuccess && d.occ[i] < 1) e = cudaErrorInvalidConfiguration;
+    }
     if (e != cudaSuccess) return e;
     d.ready = true;
   }
@@ -113,7 +124,23 @@ cudaError_t kv_prepare(int dev, KvDeviceInfo* info) {
   return cudaSuccess;
 }
 
-constexpr long long kKvPlanBytes = kKvMaxBlocks * 16;
+// What a call launches and how its workspace is laid out: the plans and the
+// partial results of both kernels.
+struct KvLayout {
+  int few, many;          // variants; many < 0: not launched
+  long long part_few, part_many, bytes;
+};
+
+KvLayout kv_layout(int D, long long rows) {
+  KvLayout l;
+  const int v0 = D == 64 ? 0 : 3;
+  l.few = rows <= 8 ? v0 : v0 + 1;
+  l.many = rows > kKvFewRows ? v0 + 2 : -1;
+  l.part_few = 32LL * (kKvMaxBlocks + kTcaMaxBlocks);
+  l.part_many = l.part_few + 2LL * kKvMaxBlocks * kv_variant(l.few).slot * 4;
+  l.bytes = l.part_many + (l.many < 0 ? 0 : 2LL * kTcaMaxBlocks * kv_variant(l.many).slot * 4);
+  return l;
+}
 
 }  // namespace
 
@@ -242,8 +269,7 @@ respin_status_t respin_kv_attention_workspace(int q_heads, int kv_heads, int hea
   if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || N < 0 || max_q < 0)
     return fail(RESPIN_ERR_INVALID_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d, N=%d and max_q=%d not negative",
                 q_heads, kv_heads, N, max_q);
-  const KvAttnVariant v = kv_pick(head_dim, kv_attn_rows(N, max_q, q_heads / kv_heads));
-  *bytes = kKvPlanBytes + 2LL * kKvMaxBlocks * v.slot * 4;
+  *bytes = kv_layout(head_dim, kv_attn_rows(N, max_q, q_heads / kv_heads)).bytes;
   return ok();
 }
 
@@ -284,7 +310,9 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   e = kv_prepare(dev, &info);
   if (e != cudaSuccess) return cuda_fail(e, "preparing kv_attn_kernel");
   const int G = q_heads / H;
-  const KvAttnVariant var = kv_pick(D, kv_attn_rows(batch->N, max_q, G));
+  const long long most = kv_attn_rows(batch->N, max_q, G);
+  const KvLayout lay = kv_layout(D, most);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
@@ -295,26 +323,44 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   a.causal = causal != 0;
   a.window = window;
   a.scale = scale * 1.44269504088896340736f;
-  a.plan = static_cast<int4*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kKvPlanBytes);
-  CUtensorMap tmK, tmV;
-  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * H * cache->page_size;
-  const uint32_t box = cache->page_size < kKvTile ? cache->page_size : kKvTile;
-  const CUtensorMapSwizzle swz = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-  if (!make_tmap_u8(&tmK, cache->k, rows, D, box, D, swz) || !make_tmap_u8(&tmV, cache->v, rows, D, box, D, swz))
-    return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
-  int occ = info.occ[kv_variant_index(D, var.rows)];
-  if (occ < 1) return fail(RESPIN_ERR_CUDA, "kv_attn_kernel does not fit this device");
-  int grid = occ * info.sms;
-  if (grid > kKvMaxBlocks) grid = kKvMaxBlocks;
+  a.few_rows = most < kKvFewRows ? static_cast<int>(most) : kKvFewRows;
+  a.others = lay.many >= 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  void* args[] = {&tmK, &tmV, &a};
-  e = launch_dependent3(var.fn, dim3(static_cast<unsigned>(grid), 1, 1), kKvThreads, var.smem, s, args);
-  if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
-  if (grid > 1) {
-    void* cargs[] = {&a};
-    const int y = var.rows * D / 4 / 128;   // a row group in one pass
-    e = launch_dependent3(var.combine, dim3(static_cast<unsigned>(grid - 1), static_cast<unsigned>(y), 1), 128, 0, s, cargs);
+
+  // Sequences of many rows, then those of few; a uniform batch has one kind.
+  KvJoin few{reinterpret_cast<int4*>(ws), reinterpret_cast<float*>(ws + lay.part_few), 0, kv_variant(lay.few).rows};
+  KvJoin many{reinterpret_cast<int4*>(ws + 32 * kKvMaxBlocks), reinterpret_cast<float*>(ws + lay.part_many), 0, kTcaGroup};
+  if (lay.many >= 0) {
+    const KvAttnVariant v = kv_variant(lay.many);
+    many.blocks = info.sms < kTcaMaxBlocks ? info.sms : kTcaMaxBlocks;
+    a.plan = const_cast<int4*>(many.plan);
+    a.part = const_cast<float*>(many.part);
+    void* args[] = {&a};
+    e = launch_dependent3(v.fn, dim3(static_cast<unsigned>(many.blocks), 1, 1), v.threads, v.smem, s, args);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_attn_tc_kernel launch");
+  }
+  if (lay.many < 0 || batch->cu != nullptr) {
+    const KvAttnVariant v = kv_variant(lay.few);
+    few.blocks = info.occ[lay.few] * info.sms < kKvMaxBlocks ? info.occ[lay.few] * info.sms : kKvMaxBlocks;
+    CUtensorMap tmK, tmV;
+    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * H * cache->page_size;
+    const uint32_t box = cache->page_size < kKvTile ? cache->page_size : kKvTile;
+    const CUtensorMapSwizzle swz = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!make_tmap_u8(&tmK, cache->k, rows, D, box, D, swz) || !make_tmap_u8(&tmV, cache->v, rows, D, box, D, swz))
+      return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
+    a.plan = const_cast<int4*>(few.plan);
+    a.part = const_cast<float*>(few.part);
+    void* args[] = {&tmK, &tmV, &a};
+    e = launch_dependent3(v.fn, dim3(static_cast<unsigned>(few.blocks), 1, 1), v.threads, v.smem, s, args);
+    if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
+  }
+  const int joins = (few.blocks > 0 ? few.blocks - 1 : 0) + (many.blocks > 0 ? many.blocks - 1 : 0);
+  if (joins > 0) {
+    void* args[] = {&a, &few, &many};
+    const int y = many.blocks > 0 ? 8 : few.rows * D / 4 / 128;
+    e = launch_dependent3(D == 64 ? reinterpret_cast<const void*>(&kv_combine_kernel<64>)
+                                  : reinterpret_cast<const void*>(&kv_combine_kernel<128>),
+                          dim3(static_cast<unsigned>(joins), static_cast<unsigned>(y), 1), 128, 0, s, args);
     if (e != cudaSuccess) return cuda_fail(e, "kv_combine_kernel launch");
   }
   return ok();

@@ -48,6 +48,7 @@ constexpr int kKvWarps = 4;          // consumer warps, 16 tokens each
 constexpr int kKvThreads = (kKvWarps + 1) * 32;
 constexpr int kKvMaxBlocks = 592;    // 4 per SM
 constexpr int kKvMinTiles = 4;       // least piece of a block
+constexpr int kKvFewRows = 16;       // rows a key head up to which a sequence is this kernel's
 constexpr float kKvBias = 6.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^14 in fp16
 constexpr float kKvLazy = 8.0f;      // the running maximum may lag by 2^8
 
@@ -60,8 +61,10 @@ struct KvAttnArgs {
   int Hq, G;             // query heads; per key head
   int causal, window;
   float scale;           // times log2 e
-  int4* plan;            // workspace: [blocks] where a block's piece begins
-  float* part;           // workspace: [blocks][2][rows][D + 2]
+  int few_rows;          // sequences of more rows (tokens * G) are another kernel's
+  int others;            // whether that kernel runs; else such a sequence is refused
+  int4* plan;            // workspace: [blocks][2] where a block's piece begins
+  float* part;           // workspace: [blocks][2] partial results
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -143,6 +146,11 @@ __device__ __forceinline__ KvScale kv_scale_of(float ks, float vs) {
   return s;
 }
 
+// Partial results: [D / 4][rows] float4, then [rows] (M, l).
+__device__ __forceinline__ void kv_put_partial(float* slot, int rows, int row, int d, float4 v) {
+  reinterpret_cast<float4*>(slot)[(d / 4) * rows + row] = v;
+}
+
 // The line of work: sequence b has units (row group, head) of `tiles` tiles
 // each, in this order.
 struct KvSeq {
@@ -158,6 +166,10 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b) {
   kv_rows(a.c, b, s.begin, end, s.len);
   const int n = end - s.begin;
   s.rows = n * a.G;
+  if (s.rows > a.few_rows) {
+    if (!a.others) record_status(kSiteKvLength);
+    s.rows = 0;
+  }
   s.groups = (s.rows + RB - 1) / RB;
   const int first = s.len - n;   // position of the first row
   const int low = a.window > 0 ? max(0, first - a.window + 1) : 0;
@@ -247,12 +259,15 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       *reinterpret_cast<volatile long long*>(sh + 4) = off;
       sh[2] = static_cast<int>(cap);
       sh[3] = static_cast<int>(chunk);
-      int4 pl = make_int4(-1, 0, 0, 0);
-      if (cap > 0) {   // where the piece begins: sequence, unit, tiles of the unit before it, chunk
+      int4 pl = make_int4(-1, 0, 0, 0), pm = make_int4(1, static_cast<int>(chunk), 0, 0);
+      if (cap > 0) {   // where the piece begins: sequence, row, head, tiles of the unit before it; its tiles
         const KvSeq s = kv_seq<C::RB>(a, b_at);
-        pl = make_int4(b_at, static_cast<int>(off / s.tiles), static_cast<int>(off % s.tiles), static_cast<int>(chunk));
+        const int unit = static_cast<int>(off / s.tiles);
+        pl = make_int4(b_at, unit / a.c.H * C::RB, unit % a.c.H, static_cast<int>(off % s.tiles));
+        pm.x = s.tiles;
       }
-      a.plan[blockIdx.x] = pl;
+      a.plan[2 * blockIdx.x] = pl;
+      a.plan[2 * blockIdx.x + 1] = pm;
     }
   }
   __syncthreads();
@@ -329,7 +344,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const int unit = static_cast<int>(off / s.tiles), t = static_cast<int>(off % s.tiles);
     const int n = min(left, s.tiles - t);
     const int h = unit % a.c.H, row0 = (unit / a.c.H) * C::RB;
-    const int first_pos = s.len - s.rows / Gq;
+    const int first_pos = s.len - s.rows / Gq;   // of the sequence's first row
 
     // Q^T fragments: row n = lane / 4 of each group of 8, scaled by a power of two
     uint32_t qf[NT][KS][2];
@@ -555,10 +570,10 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         for (int i = 0; i < D / 16; ++i) o[i] = fmaf(at[i], f, o[i]);
       }
       if (split) {
-        float* po = slot + (8 * x + row) * (D + 2);
 #pragma unroll
-        for (int i = 0; i < D / 16; i += 2) *reinterpret_cast<float2*>(po + d0 + i) = make_float2(o[i], o[i + 1]);
-        if (d0 == 0) *reinterpret_cast<float2*>(po + D) = make_float2(Mx, ls);
+        for (int i = 0; i < D / 16; i += 4)
+          kv_put_partial(slot, C::RB, 8 * x + row, d0 + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
+        if (d0 == 0) reinterpret_cast<float2*>(slot + C::RB * D)[8 * x + row] = make_float2(Mx, ls);
       } else {
         const float inv = ls > 0.0f ? __fdiv_rn(1.0f, ls) : 0.0f;   // a row that sees nothing is 0
         const long long tokr = s.begin + gr / Gq;
@@ -583,49 +598,57 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
   }
 }
 
-// Joins the partial results of units that several blocks share. Block
-// (i, y): the unit that piece i begins inside of, if piece i is the second of
-// the unit's pieces; rows y, y + gridDim.y, ...
-template <int D, int RB>
-__global__ void __launch_bounds__(128) kv_combine_kernel(const KvAttnArgs a) {
+// Joins the partial results of units that several blocks of a kernel share.
+// Block (i, y) of `blocks` pieces: the unit that piece i + 1 begins inside of,
+// if that is the second of the unit's pieces; every gridDim.y-th part of its
+// rows and dims.
+struct KvJoin {
+  const int4* plan;
+  const float* part;
+  int blocks, rows;   // pieces; rows of a partial result
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) kv_combine_kernel(const KvAttnArgs a, const KvJoin few, const KvJoin many) {
   grid_dep_wait();
   grid_dep_launch();
-  const int c = blockIdx.x + 1;
-  const int4 pl = a.plan[c];
-  if (pl.x < 0 || pl.z == 0 || pl.z > pl.w) return;   // no piece; at a unit's start; a later piece of the unit
-  const int chunk = pl.w;
-  const KvSeq s = kv_seq<RB>(a, pl.x);
-  const int h = pl.y % a.c.H, row0 = (pl.y / a.c.H) * RB;
+  const int i0 = blockIdx.x;
+  const KvJoin j = i0 < few.blocks - 1 ? few : many;
+  const int c = (i0 < few.blocks - 1 ? i0 : i0 - max(0, few.blocks - 1)) + 1;
+  const int4 pl = j.plan[2 * c], pm = j.plan[2 * c + 1];
+  const int z = pl.w, tiles = pm.x, chunk = pm.y;
+  if (pl.x < 0 || z == 0 || z > chunk) return;   // no piece; at a unit's start; a later piece of the unit
+  int begin, end, len;
+  kv_rows(a.c, pl.x, begin, end, len);
+  const int rows = (end - begin) * a.G - pl.y;
+  const int RB = j.rows;
   // pieces c - 1 (its last segment: the second slot unless the unit starts the piece), c, c + 1, ...
-  const int pieces = 1 + (s.tiles - pl.z + chunk - 1) / chunk;
+  const int pieces = 1 + (tiles - z + chunk - 1) / chunk;
   const long long slot = static_cast<long long>(RB) * (D + 2);
-  const float* first = a.part + (2LL * (c - 1) + (pl.z == chunk ? 0 : 1)) * slot;
-  const float* rest = a.part + 2LL * c * slot;
-  const int tid = threadIdx.x;
-  constexpr int T = D / 4;            // threads of a row, 4 dims each
-  constexpr int RP = 128 / T;         // rows of a pass
-  for (int row = blockIdx.y * RP + tid / T; row < RB; row += gridDim.y * RP) {
-    const int gr = row0 + row;
-    if (gr >= s.rows) break;
-    const int d0 = (tid % T) * 4;
+  const float* first = j.part + (2LL * (c - 1) + (z == chunk ? 0 : 1)) * slot;
+  const float* rest = j.part + 2LL * c * slot;
+  for (int at = blockIdx.y * 128 + threadIdx.x; at < RB * (D / 4); at += gridDim.y * 128) {
+    const int row = at % RB, d0 = at / RB * 4;
+    if (row >= rows) continue;
     float M = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int i = 0; i < pieces; ++i) {
-      const float* p = (i == 0 ? first : rest + 2LL * (i - 1) * slot) + row * (D + 2);
-      const float2 ml = *reinterpret_cast<const float2*>(p + D);
-      const float2 x = *reinterpret_cast<const float2*>(p + d0), y = *reinterpret_cast<const float2*>(p + d0 + 2);
+      const float* p = i == 0 ? first : rest + 2LL * (i - 1) * slot;
+      const float2 ml = reinterpret_cast<const float2*>(p + RB * D)[row];
+      const float4 x = reinterpret_cast<const float4*>(p)[at];
       const float Mn = fmaxf(M, ml.x);
       const float f = M == -INFINITY ? 0.0f : ex2(M - Mn), g = ml.x == -INFINITY ? 0.0f : ex2(ml.x - Mn);
       M = Mn;
       l = l * f + ml.y * g;
       o[0] = o[0] * f + x.x * g;
       o[1] = o[1] * f + x.y * g;
-      o[2] = o[2] * f + y.x * g;
-      o[3] = o[3] * f + y.y * g;
+      o[2] = o[2] * f + x.z * g;
+      o[3] = o[3] * f + x.w * g;
     }
     const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
-    const long long tok = s.begin + gr / a.G;
-    const int hq = h * a.G + gr % a.G;
+    const int gr = pl.y + row;
+    const long long tok = begin + gr / a.G;
+    const int hq = pl.z * a.G + gr % a.G;
     *reinterpret_cast<uint2*>(a.out + tok * a.ldo + static_cast<long long>(hq) * D + d0) =
         make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
     if (a.lse != nullptr && d0 == 0)

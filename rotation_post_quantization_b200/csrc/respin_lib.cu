@@ -25,6 +25,7 @@
 #include "boundary_tc.cuh"
 #include "factor_builder.h"
 #include "kv_attention.cuh"
+#include "kv_attention_tc.cuh"
 #include "kv_cache.cuh"
 #include "qk_norm_rope.cuh"
 #include "weight_tool.h"

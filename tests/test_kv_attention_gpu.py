@@ -183,3 +183,11 @@ def test_refused_indexes_are_recorded(q):
         t.copy_(keep)
     assert torch.equal(call(), good)
     assert rq.respin_device_status() == 0
+
+def test_max_q_below_the_truth_is_recorded():
+    bt = Batch([1, 40], [100, 77], 1, 128, 32, seed=13).to_gpu()
+    tq, _ = bf16(np.random.default_rng(3).standard_normal((41, 4, 128)))
+    out = torch.full((41, 4, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    rq.respin_kv_attention(bt.cache, tq, bt.t_len, bt.t_table, out, workspace(bt.cache, 4, 41, 2), cu=bt.t_cu, max_q=2)
+    assert rq.respin_device_status() == 512
+    assert (out[1:] == 7).all() and not (out[:1] == 7).all()
