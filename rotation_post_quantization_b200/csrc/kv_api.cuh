@@ -82,6 +82,21 @@ KvAttnVariant kv_many() {
           static_cast<long long>(C::SlotFloats)};
 }
 
+// 3-D tensor map over bf16 [N][heads][D] with ld elements between tokens, box
+// {D, box_heads, box_tokens}; tokens past the end read as zeros.
+bool make_tmap_heads(CUtensorMap* m, const void* ptr, int N, int heads, int D, long long ld, int box_heads, int box_tokens) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(N)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_heads > 256 ? 256 : box_heads),
+                             static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr int kKvVariants = 6;
 
 // Variants 0, 1: at most 8 rows a key head (single tokens: one n = 8 product)
@@ -330,21 +345,27 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   // Sequences of many rows, then those of few; a uniform batch has one kind.
   KvJoin few{reinterpret_cast<int4*>(ws), reinterpret_cast<float*>(ws + lay.part_few), 0, kv_variant(lay.few).rows};
   KvJoin many{reinterpret_cast<int4*>(ws + 32 * kKvMaxBlocks), reinterpret_cast<float*>(ws + lay.part_many), 0, kTcaGroup};
+  const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * H * cache->page_size;
+  const uint32_t box = cache->page_size < kKvTile ? cache->page_size : kKvTile;   // both kernels' 64-token tiles
+  CUtensorMap tmK, tmV;
   if (lay.many >= 0) {
     const KvAttnVariant v = kv_variant(lay.many);
     many.blocks = info.sms < kTcaMaxBlocks ? info.sms : kTcaMaxBlocks;
+    if (!make_tmap_u8(&tmK, cache->k, rows, D, box, D) || !make_tmap_u8(&tmV, cache->v, rows, D, box, D))
+      return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
+    const int slot_rows = kTcaSlot / (2 * D);
+    CUtensorMap tmQ;
+    if (!make_tmap_heads(&tmQ, q, batch->N, q_heads, D, ld_q, G, slot_rows % G ? 1 : slot_rows / G))
+      return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the queries");
     a.plan = const_cast<int4*>(many.plan);
     a.part = const_cast<float*>(many.part);
-    void* args[] = {&a};
+    void* args[] = {&tmQ, &tmK, &tmV, &a};
     e = launch_dependent3(v.fn, dim3(static_cast<unsigned>(many.blocks), 1, 1), v.threads, v.smem, s, args);
     if (e != cudaSuccess) return cuda_fail(e, "kv_attn_tc_kernel launch");
   }
   if (lay.many < 0 || batch->cu != nullptr) {
     const KvAttnVariant v = kv_variant(lay.few);
     few.blocks = info.occ[lay.few] * info.sms < kKvMaxBlocks ? info.occ[lay.few] * info.sms : kKvMaxBlocks;
-    CUtensorMap tmK, tmV;
-    const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * H * cache->page_size;
-    const uint32_t box = cache->page_size < kKvTile ? cache->page_size : kKvTile;
     const CUtensorMapSwizzle swz = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     if (!make_tmap_u8(&tmK, cache->k, rows, D, box, D, swz) || !make_tmap_u8(&tmV, cache->v, rows, D, box, D, swz))
       return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");

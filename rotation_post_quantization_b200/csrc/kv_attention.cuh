@@ -411,7 +411,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
 
     for (int i = 0; i < n; ++i) {
-      if (ok) ok = mbar_wait(full0 + 8 * stage, phase, kSiteKvLoad);
+      if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * stage, phase, kSiteKvLoad));
       const int tok = (s.t0 + t + i) * kKvTile + warp * 16;
       if (ok && tok <= any_hi && tok + 15 >= any_lo) {
         const KvScale sc = reinterpret_cast<const KvScale*>(smem + o_meta)[stage * 4 + warp];
@@ -522,7 +522,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+      if (lane == 0 && ok) mbar_arrive(empty0 + 8 * stage);   // (after a wait that gave up: no more signals)
       if (++stage == kKvStages) { stage = 0; phase ^= 1; }
     }
 

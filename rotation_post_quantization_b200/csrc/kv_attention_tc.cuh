@@ -5,27 +5,36 @@
 //
 // A block takes 256 rows of one key head (rows are (token, query head of the
 // group), so grouped heads share every tile of the cache) as two 128-row
-// tiles, and walks the cache in 128-token steps:
+// tiles, and walks the cache in 64-token steps:
 //   warps 0-3, 4-7   one row a thread of tile 0 / 1: S from tensor memory,
 //                    maximum, weights back to tensor memory as fp16;
-//   warps 8-11       codes from global memory to registers, widened to fp16
-//                    into shared memory (128-byte swizzle, two stages of K
-//                    and two of V);
-//   warp 12          one thread issues S = Q K^T (both from shared memory) and
+//   warps 8-11, 12-15 queries of tile 0 and K / of tile 1 and V from a ring of
+//                    8 KB slots to fp16 operand tiles (128-byte swizzle; two of
+//                    K, three of V);
+//   warp 16          one thread issues S = Q K^T (both from shared memory) and
 //                    O += P V (P from tensor memory, V with its dims
-//                    contiguous, i.e. N-major).
-// While one tile's rows are in the exponentials, the tensor core works for
-// the other. P takes the place of the S it comes from, so S of the next step
-// waits for the product that reads P. The running maximum may lag by 2^8
-// before the accumulators are rescaled, so rescaling is rare after the first
-// steps and is done by the row's own thread.
+//                    contiguous, i.e. N-major);
+//   warp 17          fills the ring: looks up page ids and scales of eight
+//                    steps at a time, copies pages and queries with tensor
+//                    copies (queries with asynchronous ones where a slot's rows
+//                    are no whole tokens), as far ahead as the ring is deep,
+//                    across units.
+// S of the next step is issued as soon as a tile's rows have read theirs, and
+// P has two places of its own, so the rows never wait for the tensor core:
+// their exponentials follow one another. (With 128-token steps S and P do not
+// both fit beside O at D = 128; P in the place of S makes each step a chain of
+// weights, product, scores: measured 5700 cycles for 128 tokens.) The running
+// maximum may lag by 2^8 before the accumulators are rescaled, so rescaling is
+// rare after the first steps and is done by the row's own thread.
 //
-// Tensor memory: S0, S1 (128 columns each, P in their first 64), O0, O1 (D
-// columns each). Shared memory at D = 128: Q 64 KB, K and V 128 KB.
+// Tensor memory: S0, S1 (64 columns each), P0, P1 (2 x 32 each), O0, O1 (D
+// each). Shared memory at D = 128: Q 64 KB, K 32 KB, V 48 KB, ring 48 KB.
 //
 // Work: as in kv_attention.cuh one line of steps cut into equal pieces, here
 // with each row group's own number of steps (causal rows see fewer).
 #pragma once
+
+#include <type_traits>
 
 #include "kv_attention.cuh"
 
@@ -33,11 +42,25 @@ namespace respin {
 
 constexpr int kTcaRows = 128;       // rows of a tile
 constexpr int kTcaGroup = 256;      // rows of a block
-constexpr int kTcaTile = 128;       // tokens of a step
-constexpr int kTcaThreads = 13 * 32;
-constexpr int kTcaMinTiles = 4;     // least piece of a block
+constexpr int kTcaTile = 64;        // tokens of a step
+constexpr int kTcaThreads = 20 * 32;
+// registers of a thread of the rows', the operands' and the last warps:
+// 2 * 120 + 2 * 72 + 96 = 5 * 96, what 640 threads are launched with
+constexpr int kTcaRegsRows = 120, kTcaRegsCodes = 72, kTcaRegsLast = 96;
+constexpr int kTcaVStages = 3;
+constexpr int kTcaMinTiles = 8;     // least piece of a block
 constexpr int kTcaMaxBlocks = 160;  // one per SM
-constexpr int kTcaMeta = 4;         // steps whose scales are kept
+constexpr int kTcaMeta = 16;        // steps whose scales are kept (the ring is at most seven ahead of the rows)
+constexpr int kTcaSlots = 6;        // of the ring
+constexpr int kTcaSlot = 8192;
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 
 // D[tmem] (+)= A[tmem] * B[smem]: A holds two 16-bit values a column.
 __device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -62,6 +85,54 @@ __host__ __device__ constexpr uint32_t umma_idesc_f16(int M, int N, bool n_major
 // 64 values of N `n_stride` bytes on.
 __device__ __forceinline__ uint64_t umma_desc_sw128_n(uint32_t smem_addr, uint32_t n_stride) {
   return (umma_desc_sw128(smem_addr) & ~(0x3FFFull << 16)) | (static_cast<uint64_t>(n_stride >> 4) << 16);
+}
+
+// A bounded wait of a whole warp: the same answer in every lane, and the warp
+// together again (lanes may leave a wait apart). A role that gives up signals
+// and issues nothing more, so the others run into their own limits and leave.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, int site) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, site));
+}
+
+// One lane of the (converged) warp, known to the compiler as one: operands of
+// the tensor-core instructions then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+template <int R>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
+// A point before which values read from tensor memory are not used.
+__device__ __forceinline__ void tmem_values(uint32_t (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(v[i]), "+r"(v[i + 1]), "+r"(v[i + 2]), "+r"(v[i + 3]), "+r"(v[i + 4]), "+r"(v[i + 5]),
+                      "+r"(v[i + 6]), "+r"(v[i + 7]));
+}
+
+// 32 bytes at once (32-byte aligned).
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// 16 bytes global -> shared by this thread (zeros where `in` is false), and an
+// arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Packed pairs of fp32.
@@ -208,28 +279,36 @@ __device__ __forceinline__ void tca_locate(const KvAttnArgs& a, volatile int* sh
 
 template <int D>
 struct TcaCfg {
-  static constexpr int Op = kTcaTile * D * 2;            // bytes of one fp16 operand tile
-  static constexpr int OQ = 0, OK = 2 * Op, OV = 4 * Op, OMeta = 6 * Op;
-  static constexpr int OBar = OMeta + kTcaMeta * 8 * 16;
-  static constexpr int Bars = 17;
+  static constexpr int OpQ = kTcaRows * D * 2, Op = kTcaTile * D * 2;   // bytes of the fp16 operand tiles
+  static constexpr int OQ = 0, OK = 2 * OpQ, OV = OK + 2 * Op, ORing = OV + kTcaVStages * Op;
+  static constexpr int OMeta = ORing + kTcaSlots * kTcaSlot;            // [steps][4] scales of 16 tokens each
+  static constexpr int OCoef = OMeta + kTcaMeta * 4 * 16;               // [2][256] the rows' factors, by unit parity
+  static constexpr int OBar = OCoef + 2 * kTcaGroup * 4;
+  static constexpr int Bars = 21 + 2 * kTcaVStages + 2 * kTcaSlots;
   static constexpr int Smem = 1024 + OBar + 8 * Bars + 64;
   static constexpr int Columns = 512;
   static constexpr int SlotFloats = kTcaGroup * (D + 2);
 };
 
+// tmQ: bf16 [N][Hq][D], box {D, G, rows of a slot / G} (not used where G does not divide those rows);
+// tmK, tmV: uint8 [pages * H * P, D], box {D, min(P, 64)}; no swizzle.
 template <int D>
-__global__ void __launch_bounds__(kTcaThreads, 1) kv_attn_tc_kernel(const KvAttnArgs a) {
+__global__ void __launch_bounds__(kTcaThreads, 1)
+kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const KvAttnArgs a) {
   using C = TcaCfg<D>;
   constexpr int KB = D / 64;         // 64-value blocks of a row
-  constexpr int Block = kTcaTile * 128;   // bytes of one block of an operand tile
+  constexpr int Block = kTcaTile * 128, BlockQ = kTcaRows * 128;   // bytes of one block of K or V, of Q
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (base - raw);
   const uint32_t bars = base + C::OBar;
-  const uint32_t kfull = bars, kempty = bars + 16, vfull = bars + 32, vempty = bars + 48;   // [2] stages
-  const uint32_t qfull = bars + 64, sfull = bars + 80, pfull = bars + 96, odone = bars + 112;   // [2] tiles
-  const uint32_t drained = bars + 128;
+  const uint32_t kfull = bars, kempty = bars + 16;                            // [2] stages
+  const uint32_t qfull = bars + 32, qempty = bars + 48, sfull = bars + 64, sfree = bars + 80;   // [2] tiles
+  const uint32_t pfull = bars + 96, pfree = bars + 128, drained = bars + 160;                // [2 tiles][2 places of P]
+  const uint32_t vfull = bars + 168, vempty = vfull + 8 * kTcaVStages;                       // stages of V
+  const uint32_t efull = vempty + 8 * kTcaVStages, eempty = efull + 8 * kTcaSlots;           // slots
   volatile int* sh = reinterpret_cast<volatile int*>(smem + C::OBar + 8 * C::Bars);
   const uint32_t tslot = base + C::OBar + 8 * C::Bars + 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -238,17 +317,27 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_attn_tc_kernel(const KvAttn
     for (int i = 0; i < 2; ++i) {
       mbar_init(kfull + 8 * i, 4);
       mbar_init(kempty + 8 * i, 1);
+      mbar_init(qfull + 8 * i, 4);
+      mbar_init(qempty + 8 * i, 1);
+      mbar_init(sfull + 8 * i, 2);   // the product, and the issuing thread (it saw the step's scales)
+      mbar_init(sfree + 8 * i, 4);
+      mbar_init(pfull + 16 * i, 4);
+      mbar_init(pfull + 16 * i + 8, 4);
+      mbar_init(pfree + 16 * i, 1);
+      mbar_init(pfree + 16 * i + 8, 1);
+    }
+    for (int i = 0; i < kTcaVStages; ++i) {
       mbar_init(vfull + 8 * i, 4);
       mbar_init(vempty + 8 * i, 1);
-      mbar_init(qfull + 8 * i, 4);
-      mbar_init(sfull + 8 * i, 2);   // the product, and the issuing thread (it saw the step's scales)
-      mbar_init(pfull + 8 * i, 4);
-      mbar_init(odone + 8 * i, 1);
+    }
+    for (int i = 0; i < kTcaSlots; ++i) {
+      mbar_init(efull + 8 * i, 32);   // every lane of warp 17, and the bytes of its tensor copies
+      mbar_init(eempty + 8 * i, 4);
     }
     mbar_init(drained, 1);
     fence_mbarrier_init();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tslot, C::Columns);
     tmem_relinquish();
   }
@@ -272,12 +361,16 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_attn_tc_kernel(const KvAttn
 
   if (warp < 8) {
     // ------------------------------------------------ rows: weights
+    regs_take<kTcaRegsRows>();
     const int tile = warp >> 2, r = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 lanes of tensor memory a warp
-    const uint32_t ts = tmem + lanes + tile * 128, to = tmem + lanes + 256 + tile * D;
+    const uint32_t ts = tmem + lanes + tile * 64, tp = tmem + lanes + 128 + tile * 64, to = tmem + lanes + 256 + tile * D;
     bool ok = true;
-    int ph_s = 0, ph_o = 0, step = 0, seg = 0;
-    while (cur.left > 0) {
+    int use = 0, step = 0, seg = 0;   // use: steps of this tile; P's place is use & 1
+    const uint32_t pfree_t = pfree + 16 * tile;
+    // PV of use u has completed (its P is free, its O is there): u the last or the one before
+    auto product = [&](int u) { return mbar_wait_warp(pfree_t + 8 * (u & 1), (u >> 1) & 1, kSiteKvAccum); };
+    while (cur.left > 0 && ok) {
       const int n = cur.steps();
       const int row0 = cur.g * kTcaGroup;
       if (row0 + tile * kTcaRows < cur.s.rows) {
@@ -288,134 +381,120 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_attn_tc_kernel(const KvAttn
         const int pos = cur.s.len - cur.s.n + tok;
         const int hi = a.causal ? min(pos, cur.s.len - 1) : cur.s.len - 1;
         const int lo = a.window > 0 ? pos - a.window + 1 : 0;
-        // ---- Q: scaled by a power of two to fp16
-        float coef;
-        {
-          const uint4* qp = reinterpret_cast<const uint4*>(a.q + (cur.s.begin + tok) * a.ldq + static_cast<long long>(hq) * D);
-          uint8_t* qs = smem + C::OQ + tile * C::Op + (r >> 3) * 1024 + (r & 7) * 128;
-          uint4 w[D / 8];
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) w[i] = live ? qp[i] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) m = max(m, bf16x8_finite_amax(w[i]));
-          const int e = max(-110, static_cast<int>(m >> 7) - 127);
-          const float up = __int_as_float((14 - e + 127) << 23);
-          coef = __int_as_float((e - 14 + 127) << 23) * a.scale;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            float f[8];
-            bf16x8_to_f32(w[i], f);
-            const uint4 v = make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
-                                       pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
-            *reinterpret_cast<uint4*>(qs + (i >> 3) * Block + (((i & 7) ^ (r & 7)) << 4)) = v;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(qfull + 8 * tile);
-        }
-        float M = -INFINITY, l = 0.0f;
-        for (int j = 0; j < n; ++j) {
-          if (ok) ok = mbar_wait(sfull + 8 * tile, ph_s, kSiteKvAccum);
-          ph_s ^= 1;
+        float M = -INFINITY, l = 0.0f, coef = 0.0f;
+        for (int j = 0; j < n; ++j, ++use) {
+          ok = mbar_wait_warp(sfull + 8 * tile, use & 1, kSiteKvAccum);
+          if (!ok) break;
           tc_fence_after();
+          uint32_t v[2][32];
+          tmem_ld_32x32b_x32(ts, v[0]);
+          tmem_ld_32x32b_x32(ts + 32, v[1]);
+          if (j == 0) coef = reinterpret_cast<const float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r];
           const int t = (cur.t0 + cur.z + j) * kTcaTile;
-          const KvScale* meta = reinterpret_cast<const KvScale*>(smem + C::OMeta) + ((step + j) % kTcaMeta) * 8;
+          const KvScale* meta = reinterpret_cast<const KvScale*>(smem + C::OMeta) + ((step + j) % kTcaMeta) * 4;
           const bool whole = __all_sync(0xFFFFFFFFu, t >= lo && t + kTcaTile - 1 <= hi);
-          // ---- maximum of the exponents
+          tmem_wait_ld();
+          tmem_values(v[0]);
+          tmem_values(v[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfree + 8 * tile);
+          __syncwarp();
+          if (!whole) {
+            const int first = lo - t, last = hi - t;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i < first || 32 * c + i > last) v[c][i] = 0xFF800000u;   // -inf
+          }
+          // ---- maximum of the exponents: of each 16 tokens' products, then with their scales. A
+          // factor of 0 (all products are 0, or are to count as 0) becomes one that keeps -inf.
           float mx = -INFINITY;
+          float ck[4], of[4], iv[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld_32x32b_x32(ts + 32 * c, v);
-            tmem_wait_ld();
+            const KvScale sc = meta[c];
+            const uint32_t* x = &v[c / 2][16 * (c % 2)];
+            float m[4];
 #pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-              const KvScale sc = meta[2 * c + hb];
-              const float ck = coef * sc.k;
-              const uint64_t ck2 = f32x2(ck, ck), lv2 = f32x2(sc.lv, sc.lv);
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                float2 e = f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[16 * hb + i]), __uint_as_float(v[16 * hb + i + 1])), ck2, lv2));
-                if (!whole) {
-                  const int at = t + 32 * c + 16 * hb + i;
-                  if (at > hi || at < lo) e.x = -INFINITY;
-                  if (at + 1 > hi || at + 1 < lo) e.y = -INFINITY;
-                }
-                mx = fmaxf(mx, fmaxf(e.x, e.y));
-              }
-            }
+            for (int i = 0; i < 4; ++i)
+              m[i] = fmaxf(fmaxf(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
+                           fmaxf(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
+            const float m4 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+            ck[c] = fmaxf(coef * sc.k, 1e-37f);
+            of[c] = sc.lv;
+            iv[c] = sc.iv;
+            mx = fmaxf(mx, fmaf(m4, ck[c], sc.lv));
           }
           if (__any_sync(0xFFFFFFFFu, mx > M + (kKvBias + kKvLazy))) {
             const float Mn = mx > M + (kKvBias + kKvLazy) ? mx - kKvBias : M;
             const float f = Mn == M ? 1.0f : ex2(M - Mn);   // 0 from nothing
             M = Mn;
             l *= f;
-            if (j > 0) {   // the products before this S are complete
+            if (j > 0) {
+              ok = product(use - 1);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32], u[16];
-                tmem_ld_32x32b_x32(to + 32 * c, v);
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t u[16];
+                tmem_ld_32x32b_x16(to + 16 * c, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                tmem_st_32x32b_x16(to + 32 * c, u);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(v[16 + i]) * f);
-                tmem_st_32x32b_x16(to + 32 * c + 16, u);
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+                tmem_st_32x32b_x16(to + 16 * c, u);
               }
             }
           }
           // ---- weights, their sum, and P
           const float Ms = M == -INFINITY ? 0.0f : M;
+          if (use >= 2) ok = product(use - 2);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], p[16];
-            tmem_ld_32x32b_x32(ts + 32 * c, v);
-            tmem_wait_ld();
+          for (int c = 0; c < 2; ++c) {
+            uint32_t p[16];
 #pragma unroll
             for (int hb = 0; hb < 2; ++hb) {
-              const KvScale sc = meta[2 * c + hb];
-              const float ck = coef * sc.k, of = sc.lv - Ms;
-              const uint64_t ck2 = f32x2(ck, ck), of2 = f32x2(of, of);
-              uint64_t sum = 0;
+              const float o = of[2 * c + hb] - Ms;
+              const uint64_t ck2 = f32x2(ck[2 * c + hb], ck[2 * c + hb]), of2 = f32x2(o, o);
+              uint64_t sum[2] = {0, 0};
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
-                float2 e = f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[16 * hb + i]), __uint_as_float(v[16 * hb + i + 1])), ck2, of2));
-                if (!whole) {
-                  const int at = t + 32 * c + 16 * hb + i;
-                  if (at > hi || at < lo) e.x = -INFINITY;
-                  if (at + 1 > hi || at + 1 < lo) e.y = -INFINITY;
-                }
+                const float2 e = f32x2_split(fma_f32x2(
+                    f32x2(__uint_as_float(v[c][16 * hb + i]), __uint_as_float(v[c][16 * hb + i + 1])), ck2, of2));
                 const float x = ex2(e.x), y = ex2(e.y);
-                sum = add_f32x2(sum, f32x2(x, y));
+                sum[(i / 2) & 1] = add_f32x2(sum[(i / 2) & 1], f32x2(x, y));
                 p[8 * hb + i / 2] = pack_f16x2(x, y);
               }
-              const float2 s2 = f32x2_split(sum);
-              l = fmaf(s2.x + s2.y, sc.iv, l);
+              const float2 s2 = f32x2_split(add_f32x2(sum[0], sum[1]));
+              l = fmaf(s2.x + s2.y, iv[2 * c + hb], l);
             }
-            tmem_st_32x32b_x16(ts + 16 * c, p);
+            tmem_st_32x32b_x16(tp + 32 * (use & 1) + 16 * c, p);
           }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + 8 * tile);
-          // the phase of odone for this step passes whether or not it is waited for
-          if (j + 1 < n) ph_o ^= 1;
+          if (lane == 0) mbar_arrive(pfull + 16 * tile + 8 * (use & 1));
+          __syncwarp();
         }
-        if (ok) ok = mbar_wait(odone + 8 * tile, ph_o, kSiteKvAccum);
-        ph_o ^= 1;
+        if (ok) ok = product(use - 1);
+        if (!ok) break;
         tc_fence_after();
         const bool split = n < cur.tiles;
         float* slot = a.part + (static_cast<long long>(blockIdx.x) * 2 + (seg > 0 ? 1 : 0)) * C::SlotFloats;
         const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
         __nv_bfloat16* op = a.out + (cur.s.begin + tok) * a.ldo + static_cast<long long>(hq) * D;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.out) | (a.ldo * 2)) % 32 == 0;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
+          __syncwarp();   // absent rows skip the stores
           tmem_ld_32x32b_x32(to + 32 * c, v);
           tmem_wait_ld();
-          if (!live || !ok) continue;
+          tmem_values(v);
+          if (!live) continue;
           if (split) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -424,17 +503,24 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_attn_tc_kernel(const KvAttn
                                          __uint_as_float(v[i + 3])));
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t w[4];
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t w[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
+              for (int k = 0; k < 8; ++k)
                 w[k] = pack_bf16x2(__uint_as_float(v[i + 2 * k]) * inv, __uint_as_float(v[i + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(op + 32 * c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+              uint32_t* at = reinterpret_cast<uint32_t*>(op + 32 * c + i);
+              if (wide) {
+                st_global_v8(at, w);
+              } else {
+                reinterpret_cast<uint4*>(at)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(at)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              }
             }
           }
         }
+        __syncwarp();
         tc_fence_before();
-        if (live && ok) {
+        if (live) {
           if (split)
             reinterpret_cast<float2*>(slot + kTcaGroup * D)[row - row0] = make_float2(M, l);
           else if (a.lse != nullptr)
@@ -446,143 +532,313 @@ __global__ void __launch_bounds__(kTcaThreads, 1) kv_attn_tc_kernel(const KvAttn
       ++seg;
       cur.next(a);
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ------------------------------------------------ codes to fp16
-    const int pt = tid - 256;
-    constexpr int Pieces = D / 16;                 // 16-byte pieces of a token's codes
-    constexpr int Per = kTcaTile * Pieces / 128;   // pieces of a thread
-    constexpr int Step = 128 / Pieces;             // tokens between them
-    const int c = pt % Pieces, tk = pt / Pieces;
+    regs_give<kTcaRegsCodes>();
+    const int pt = (tid - 256) & 127, half = (warp - 8) >> 2;   // half: 0 tile 0 and K, 1 tile 1 and V
     bool ok = true;
-    int step = 0;
-    while (cur.left > 0) {
-      const int n = cur.steps();
-      // lane l < 8: the 16 tokens from 16 l on of a step
-      auto look = [&](int j, int& row, KvScale& sc) {
-        row = -1;
-        sc = kv_scale_of(0.0f, 0.0f);
-        sc.lv = -INFINITY;
-        const int t = (cur.t0 + cur.z + j) * kTcaTile + 16 * lane;
-        if (j < n && lane < 8 && t < cur.s.len) {
-          const int page = kv_page(a.c, cur.b, t);
-          if (page >= 0) {
-            const int phd = page * a.c.H + cur.h;
-            row = phd * a.c.P + t % a.c.P;
-            if (warp == 8) sc = kv_scale_of(a.c.k_scale[phd], a.c.v_scale[phd]);
-          }
-        }
-      };
-      auto fetch = [&](const int8_t* codes, int row, uint4 (&w)[Per]) {
-#pragma unroll
-        for (int i = 0; i < Per; ++i) {
-          const int t = tk + Step * i;
-          const int rw = __shfl_sync(0xFFFFFFFFu, row, t / 16);
-          w[i] = make_uint4(0u, 0u, 0u, 0u);   // tokens of no page: zeros, whatever weight is 0 times them
-          if (rw >= 0) w[i] = reinterpret_cast<const uint4*>(codes + static_cast<long long>(rw + t % 16) * D)[c];
-        }
-      };
-      auto widen = [&](uint8_t* to, const uint4 (&w)[Per]) {
-#pragma unroll
-        for (int i = 0; i < Per; ++i) {
-          const int t = tk + Step * i;
-          uint8_t* p = to + (c >> 2) * Block + (t >> 3) * 1024 + (t & 7) * 128;
-          const uint32_t x[4] = {w[i].x ^ 0x80808080u, w[i].y ^ 0x80808080u, w[i].z ^ 0x80808080u, w[i].w ^ 0x80808080u};
-          const uint4 lo = make_uint4(codes_f16x2<0>(x[0]), codes_f16x2<1>(x[0]), codes_f16x2<0>(x[1]), codes_f16x2<1>(x[1]));
-          const uint4 hi = make_uint4(codes_f16x2<0>(x[2]), codes_f16x2<1>(x[2]), codes_f16x2<0>(x[3]), codes_f16x2<1>(x[3]));
-          const int p0 = 2 * (c & 3);
-          // the two blocks of a row lie on the same banks: their lanes store the other half first
-          const bool flip = c >= 4;
-          *reinterpret_cast<uint4*>(p + (((flip ? p0 + 1 : p0) ^ (t & 7)) << 4)) = flip ? hi : lo;
-          *reinterpret_cast<uint4*>(p + (((flip ? p0 : p0 + 1) ^ (t & 7)) << 4)) = flip ? lo : hi;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      };
-      int row, row_n;
-      KvScale sc, sc_n;
-      uint4 wk[Per], wv[Per];
-      look(0, row, sc);
-      fetch(a.c.k, row, wk);
-      for (int j = 0; j < n; ++j, ++step) {
-        const int st = step & 1, par = ((step >> 1) & 1) ^ 1;
-        fetch(a.c.v, row, wv);
-        look(j + 1, row_n, sc_n);
-        if (ok) ok = mbar_wait(kempty + 8 * st, par, kSiteKvFree);
-        if (warp == 8 && lane < 8)
-          reinterpret_cast<KvScale*>(smem + C::OMeta)[(step % kTcaMeta) * 8 + lane] = sc;
-        widen(smem + C::OK + st * C::Op, wk);
-        if (lane == 0) mbar_arrive(kfull + 8 * st);
-        if (j + 1 < n) fetch(a.c.k, row_n, wk);
-        if (ok) ok = mbar_wait(vempty + 8 * st, par, kSiteKvFree);
-        widen(smem + C::OV + st * C::Op, wv);
-        if (lane == 0) mbar_arrive(vfull + 8 * st);
-        row = row_n;
-        sc = sc_n;
+    int seg = 0, slot = 0, ph_e = 0, ph_q = 1, stage = 0, ph_s = 1;
+    const int stages = half ? kTcaVStages : 2;
+    auto skip = [&](int n) {   // entries of the other half
+      slot += n;
+      while (slot >= kTcaSlots) {
+        slot -= kTcaSlots;
+        ph_e ^= 1;
       }
-      cur.next(a);
-    }
-  } else if (lane == 0) {
-    // ------------------------------------------------ tensor core
-    constexpr uint32_t is = umma_idesc_f16(kTcaRows, kTcaTile, false), io = umma_idesc_f16(kTcaRows, D, true);
-    bool ok = true;
-    int step = 0, ph_q[2] = {0, 0}, ph_p[2] = {0, 0}, ph_o[2] = {0, 0};
-    auto scores = [&](int tile, int st) {
-      tc_fence_after();
+    };
+    auto take = [&]() {
+      ok = ok && mbar_wait_warp(efull + 8 * slot, ph_e, kSiteKvLoad);
+      return smem + C::ORing + slot * kTcaSlot;
+    };
+    // the operand tile is written (and the slot's bytes are read): for the async proxy, then the next user
+    auto give = [&](uint32_t full) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(eempty + 8 * slot);
+        if (full) mbar_arrive(full);
+      }
+      skip(1);
+    };
+    auto widen = [&](uint8_t* to, const uint8_t* from) {
+      constexpr int Pieces = D / 16;                 // 16-byte pieces of a token's codes
+      constexpr int Per = kTcaTile * Pieces / 128;   // pieces of a thread
+      constexpr int Step = 128 / Pieces;             // tokens between them
+      const int c = pt % Pieces, tk = pt / Pieces;
+      // the two blocks of a row lie on the same banks: their lanes store the other half first
+      const bool flip = c >= 4;
+      uint8_t* p = to + (c >> 2) * Block + (tk >> 3) * 1024 + (tk & 7) * 128;   // t & 7 = tk & 7
+      const int a0 = (((2 * (c & 3)) + (flip ? 1 : 0)) ^ (tk & 7)) << 4, a1 = a0 ^ 16;
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tc_mma_bf16(tmem + tile * 128, umma_desc_sw128(base + C::OQ + tile * C::Op + kb * Block + 32 * k),
-                      umma_desc_sw128(base + C::OK + st * C::Op + kb * Block + 32 * k), is, kb + k > 0);
-      mbar_arrive(sfull + 8 * tile);
-      tc_commit(sfull + 8 * tile);
+      for (int i = 0; i < Per; ++i) {
+        const uint4 w = reinterpret_cast<const uint4*>(from)[pt + 128 * i];
+        const uint32_t x[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
+        const uint4 lo = make_uint4(codes_f16x2<0>(x[0]), codes_f16x2<1>(x[0]), codes_f16x2<0>(x[1]), codes_f16x2<1>(x[1]));
+        const uint4 hi = make_uint4(codes_f16x2<0>(x[2]), codes_f16x2<1>(x[2]), codes_f16x2<0>(x[3]), codes_f16x2<1>(x[3]));
+        *reinterpret_cast<uint4*>(p + i * Step * 128 + a0) = flip ? hi : lo;
+        *reinterpret_cast<uint4*>(p + i * Step * 128 + a1) = flip ? lo : hi;
+      }
     };
     while (cur.left > 0 && ok) {
       const int n = cur.steps();
-      const int nt = cur.g * kTcaGroup + kTcaRows < cur.s.rows ? 2 : 1;
-      ok = mbar_wait(kfull + 8 * (step & 1), (step >> 1) & 1, kSiteKvLoad);
-      for (int t = 0; t < nt && ok; ++t) {
-        ok = mbar_wait(qfull + 8 * t, ph_q[t], kSiteKvLoad);
-        ph_q[t] ^= 1;
-        if (ok) scores(t, step & 1);
-      }
-      if (ok) tc_commit(kempty + 8 * (step & 1));
-      for (int j = 0; j < n && ok; ++j, ++step) {
-        const int st = step & 1, nx = (step + 1) & 1;
-        ok = mbar_wait(vfull + 8 * st, (step >> 1) & 1, kSiteKvLoad);
-        for (int t = 0; t < nt && ok; ++t) {
-          ok = mbar_wait(pfull + 8 * t, ph_p[t], kSiteKvAccum);
-          ph_p[t] ^= 1;
+      // ---- queries: scaled by a power of two to fp16
+      constexpr int L = D / 8, RE = kTcaSlot / (2 * D);   // pieces of a row, rows of a slot
+      constexpr int Entries = kTcaRows / RE;   // of a tile
+      const int tile = half, row0 = cur.g * kTcaGroup;
+      if (half == 1) skip(Entries);
+      if (row0 + tile * kTcaRows < cur.s.rows) {
+        ok = mbar_wait_warp(qempty + 8 * tile, ph_q, kSiteKvFree);
+        ph_q ^= 1;
+#pragma unroll 1
+        for (int r0 = 0; r0 < kTcaRows; r0 += RE) {
+          const uint8_t* from = take();
           if (!ok) break;
-          tc_fence_after();
+          const int li = pt % L;
 #pragma unroll
-          for (int k = 0; k < kTcaTile / 16; ++k)
-            tc_mma_f16_ta(tmem + 256 + t * D, tmem + t * 128 + 8 * k,
-                          umma_desc_sw128_n(base + C::OV + st * C::Op + 2048 * k, Block), io, j + k > 0);
-          tc_commit(odone + 8 * t);
-          if (j + 1 < n) {
-            if (t == 0) ok = mbar_wait(kfull + 8 * nx, ((step + 1) >> 1) & 1, kSiteKvLoad);
-            if (ok) ok = mbar_wait(odone + 8 * t, ph_o[t], kSiteKvAccum);   // S takes the place of P
-            if (ok) scores(t, nx);
+          for (int i = 0; i < RE * L / 128; ++i) {
+            const int r = r0 + pt / L + 128 / L * i;
+            const uint4 w = reinterpret_cast<const uint4*>(from)[pt + 128 * i];
+            uint32_t m = bf16x8_finite_amax(w);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const int e = max(-110, static_cast<int>(m >> 7) - 127);
+            // a negative scale goes with the queries, so that the factors are not negative
+            const float up = copysignf(__int_as_float((14 - e + 127) << 23), a.scale);
+            float f[8];
+            bf16x8_to_f32(w, f);
+            *reinterpret_cast<uint4*>(smem + C::OQ + tile * C::OpQ + (li >> 3) * BlockQ + (r >> 3) * 1024 + (r & 7) * 128 +
+                                      (((li & 7) ^ (r & 7)) << 4)) =
+                make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
+                           pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
+            if (li == 0)
+              reinterpret_cast<float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r] =
+                  __int_as_float((e - 14 + 127) << 23) * fabsf(a.scale);
           }
-          ph_o[t] ^= 1;
-        }
-        if (ok) {
-          tc_commit(vempty + 8 * st);
-          if (j + 1 < n) tc_commit(kempty + 8 * nx);
+          give(r0 + RE >= kTcaRows ? qfull + 8 * tile : 0u);
         }
       }
+      if (half == 0 && row0 + kTcaRows < cur.s.rows) skip(Entries);
+      // ---- codes
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j) {
+        if (half == 1) skip(1);
+        const uint8_t* from = take();
+        const uint32_t full = (half ? vfull : kfull) + 8 * stage, empty = (half ? vempty : kempty) + 8 * stage;
+        ok = ok && mbar_wait_warp(empty, ph_s, kSiteKvFree);
+        if (!ok) break;
+        widen(smem + (half ? C::OV : C::OK) + stage * C::Op, from);
+        give(full);
+        if (half == 0) skip(1);
+        if (++stage == stages) {
+          stage = 0;
+          ph_s ^= 1;
+        }
+      }
+      ++seg;
       cur.next(a);
     }
-    // nothing issued here may still run when the tensor memory is given back
-    tc_commit(drained);
-    mbar_wait(drained, 0, kSiteKvAccum);
+  } else {
+    regs_give<kTcaRegsLast>();
+    if (warp == 17) {
+      // ---------------------------------------------- the ring
+      bool ok = true;
+      int j = 0, slot = 0, ph_e = 1, step = 0, used = 0;
+      auto turn = [&]() {
+        if (++slot == kTcaSlots) {
+          slot = 0;
+          ph_e ^= 1;
+        }
+        ++used;
+      };
+      TcaCursor ahead = cur;   // the lookups' cursor; cur: the copies'
+      int aj = 0;
+      while (cur.left > 0 && ok) {
+        // ---- page ids and scales of eight steps: lane / 4, 16 tokens a lane
+        int b = -1, h = 0, t = 0;
+#pragma unroll 1
+        for (int u = 0; u < 8 && ahead.left > 0; ++u) {
+          if (lane >> 2 == u) {
+            b = ahead.b;
+            h = ahead.h;
+            t = (ahead.t0 + ahead.z + aj) * kTcaTile + 16 * (lane & 3);
+            if (t >= ahead.s.len) b = -1;
+          }
+          if (++aj == ahead.steps()) {
+            aj = 0;
+            ahead.next(a);
+          }
+        }
+        int row = -1;
+        float ks = 0.0f, vs = 0.0f;
+        if (b >= 0) {
+          const int page = kv_page(a.c, b, t);
+          if (page >= 0) {
+            const int phd = page * a.c.H + h;
+            row = phd * a.c.P + t % a.c.P;
+            ks = a.c.k_scale[phd];
+            vs = a.c.v_scale[phd];
+          }
+        }
+        KvScale sc = kv_scale_of(ks, vs);
+        if (row < 0) sc.lv = -INFINITY;
+        // a page's first 16 tokens name its copy; tokens of no page keep what the slot holds (finite codes)
+        const int SP = min(a.c.P, kTcaTile);   // rows of a copy
+        const bool boxes = row >= 0 && ((lane & 3) * 16) % SP == 0;
+        // ---- copies, step by step
+#pragma unroll 1
+        for (int u = 0; u < 8 && cur.left > 0 && ok; ++u, ++step) {
+          if (j == 0) {
+            constexpr int L = D / 8, RE = kTcaSlot / (2 * D);
+#pragma unroll 1
+            for (int r0 = 0; r0 < kTcaGroup && ok; r0 += RE) {
+              const int row0 = cur.g * kTcaGroup + r0;
+              if (cur.g * kTcaGroup + (r0 & ~(kTcaRows - 1)) >= cur.s.rows) break;
+              ok = mbar_wait_warp(eempty + 8 * slot, ph_e, kSiteKvFree);
+              if (!ok) break;
+              const uint32_t dst = base + C::ORing + slot * kTcaSlot;
+              if (RE % a.G == 0) {   // whole tokens: rows behind the sequence are anybody's, and dead
+                if (lane == 0) {
+                  mbar_arrive_expect_tx(efull + 8 * slot, kTcaSlot);
+                  tma_load_3d(dst, &tmQ, 0, cur.h * a.G, cur.s.begin + row0 / a.G, efull + 8 * slot);
+                } else {
+                  mbar_arrive(efull + 8 * slot);
+                }
+              } else {
+                int tok = (row0 + lane / L) / a.G, g = (row0 + lane / L) % a.G;
+                const int dt = (32 / L) / a.G, dg = (32 / L) % a.G;
+#pragma unroll 1
+                for (int i = 0; i < RE * L / 32; ++i) {
+                  const bool in = tok < cur.s.n;
+                  cp_async_16(dst + (32 * i + lane) * 16,
+                              reinterpret_cast<const uint4*>(a.q + (cur.s.begin + (in ? tok : 0)) * a.ldq +
+                                                             static_cast<long long>(cur.h * a.G + g) * D) + lane % L,
+                              in);
+                  tok += dt;
+                  g += dg;
+                  if (g >= a.G) {
+                    g -= a.G;
+                    ++tok;
+                  }
+                }
+                cp_async_arrive(efull + 8 * slot);
+              }
+              turn();
+            }
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2 && ok; ++kv) {
+            ok = mbar_wait_warp(eempty + 8 * slot, ph_e, kSiteKvFree);
+            if (!ok) break;
+            const bool mine = boxes && lane >> 2 == u;
+            if (kv == 0 && lane >> 2 == u)
+              reinterpret_cast<KvScale*>(smem + C::OMeta)[(step % kTcaMeta) * 4 + (lane & 3)] = sc;
+            if (mine) mbar_arrive_expect_tx(efull + 8 * slot, static_cast<uint32_t>(SP * D));
+            if (mine)
+              tma_load_2d(base + C::ORing + slot * kTcaSlot + (lane & 3) * 16 * D, kv == 0 ? &tmK : &tmV, 0, row, efull + 8 * slot);
+            if (!mine) mbar_arrive(efull + 8 * slot);
+            turn();
+          }
+          if (++j == cur.steps()) {
+            j = 0;
+            cur.next(a);
+          }
+        }
+      }
+      // leave only once the last copies have landed, whatever became of the others
+      for (int i = max(0, used - kTcaSlots); i < used; ++i)
+        mbar_wait(efull + 8 * (i % kTcaSlots), (i / kTcaSlots) & 1, kSiteKvLoad);
+    } else if (warp == 16 && elect_one()) {
+      // ---------------------------------------------- tensor core
+      constexpr uint32_t is = umma_idesc_f16(kTcaRows, kTcaTile, false), io = umma_idesc_f16(kTcaRows, D, true);
+      // This thread's own time bounds the kernel where it is long (24 products
+      // and 6 commits a step), so what a step needs is kept in a few scalars.
+      bool ok = true;
+      uint32_t ph_q0 = 0, ph_q1 = 0;                     // units of the tiles
+      uint32_t s0 = 0, s1 = 0, p0 = 0, p1 = 0;           // scores and products of the tiles issued
+      struct At {
+        int step, tiles;      // step of the piece; tiles it has (0: none)
+        bool first, last;     // of its unit
+      };
+      int j = 0, n = cur.steps();
+      auto tiles_of = [&]() { return cur.g * kTcaGroup + kTcaRows < cur.s.rows ? 2 : 1; };
+      const uint64_t dq = umma_desc_sw128(base + C::OQ), dk = umma_desc_sw128(base + C::OK);   // addresses in 16 bytes
+      const uint64_t dv = umma_desc_sw128_n(base + C::OV, Block);
+      auto scores = [&](auto tile, const At& x) {
+        constexpr int t = decltype(tile)::value;
+        if (!ok || t >= x.tiles) return;
+        uint32_t& done = t ? s1 : s0;
+        const int st = x.step & 1;
+        if (t == 0) ok = mbar_wait(kfull + 8 * st, (x.step >> 1) & 1, kSiteKvLoad);
+        if (x.first) {
+          uint32_t& ph = t ? ph_q1 : ph_q0;
+          ok = ok && mbar_wait(qfull + 8 * t, ph, kSiteKvLoad);
+          ph ^= 1;
+        }
+        if (done > 0) ok = ok && mbar_wait(sfree + 8 * t, (done - 1) & 1, kSiteKvAccum);   // the last S is read
+        ++done;
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dks = dk + st * (C::Op >> 4);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma_bf16(tmem + t * 64, dq + t * (C::OpQ >> 4) + kb * (BlockQ >> 4) + 2 * k,
+                        dks + kb * (Block >> 4) + 2 * k, is, kb + k > 0);
+        mbar_arrive(sfull + 8 * t);
+        tc_commit(sfull + 8 * t);
+        if (x.last) tc_commit(qempty + 8 * t);
+        if (t == x.tiles - 1) tc_commit(kempty + 8 * st);
+      };
+      auto product = [&](auto tile, const At& x) {
+        constexpr int t = decltype(tile)::value;
+        if (!ok || t >= x.tiles) return;
+        const uint32_t use = t ? p1++ : p0++;
+        const int st = x.step % kTcaVStages, pb = use & 1;
+        if (t == 0) ok = mbar_wait(vfull + 8 * st, (x.step / kTcaVStages) & 1, kSiteKvLoad);
+        ok = ok && mbar_wait(pfull + 16 * t + 8 * pb, (use >> 1) & 1, kSiteKvAccum);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t dvs = dv + st * (C::Op >> 4);
+#pragma unroll
+        for (int k = 0; k < kTcaTile / 16; ++k)
+          tc_mma_f16_ta(tmem + 256 + t * D, tmem + 128 + t * 64 + 32 * pb + 8 * k, dvs + 128 * k, io, !x.first || k > 0);
+        tc_commit(pfree + 16 * t + 8 * pb);
+        if (t == x.tiles - 1) tc_commit(vempty + 8 * st);
+      };
+      const std::integral_constant<int, 0> t0{};
+      const std::integral_constant<int, 1> t1{};
+      // In time: the tiles run half a step apart.
+      At before{-1, 0, false, false}, now{0, cur.left > 0 ? tiles_of() : 0, true, n == 1};
+      scores(t0, now);
+      scores(t1, now);
+      while (ok && (now.tiles > 0 || before.tiles > 0)) {
+        At next{now.step + 1, now.tiles, false, false};
+        if (now.tiles > 0 && ++j == n) {   // the next unit's first step
+          cur.next(a);
+          j = 0;
+          n = cur.steps();
+          next.tiles = cur.left > 0 ? tiles_of() : 0;
+          next.first = true;
+        }
+        next.last = j == n - 1;
+        scores(t0, next);
+        product(t1, before);
+        scores(t1, next);
+        product(t0, now);
+        before = now;
+        now = next;
+      }
+      // nothing issued here may still run when the tensor memory is given back
+      tc_commit(drained);
+      mbar_wait(drained, 0, kSiteKvAccum);
+    }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, C::Columns);
+  if (warp == 16) tmem_dealloc(tmem, C::Columns);
 }
 
 }  // namespace respin
