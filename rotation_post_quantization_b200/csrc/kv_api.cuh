@@ -338,6 +338,7 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   a.causal = causal != 0;
   a.window = window;
   a.scale = scale * 1.44269504088896340736f;
+  a.div_g = G == 1 ? 0ull : ~0ull / static_cast<unsigned long long>(G) + 1ull;
   a.few_rows = most < kKvFewRows ? static_cast<int>(most) : kKvFewRows;
   a.others = lay.many >= 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

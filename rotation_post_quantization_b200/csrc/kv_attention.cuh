@@ -61,11 +61,18 @@ struct KvAttnArgs {
   int Hq, G;             // query heads; per key head
   int causal, window;
   float scale;           // times log2 e
+  unsigned long long div_g;   // ceil(2^64 / G), 0 for G = 1
   int few_rows;          // sequences of more rows (tokens * G) are another kernel's
   int others;            // whether that kernel runs; else such a sequence is refused
   int4* plan;            // workspace: [blocks][2] where a block's piece begins
   float* part;           // workspace: [blocks][2] partial results
 };
+
+// n / G, n >= 0: the multiplier is off by less than G / 2^64 of itself, so the
+// product's integer part is exact for any 32-bit n.
+__device__ __forceinline__ int kv_div_g(const KvAttnArgs& a, int n) {
+  return a.div_g == 0 ? n : static_cast<int>(__umul64hi(static_cast<unsigned long long>(n), a.div_g));
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -259,7 +266,8 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       *reinterpret_cast<volatile long long*>(sh + 4) = off;
       sh[2] = static_cast<int>(cap);
       sh[3] = static_cast<int>(chunk);
-      int4 pl = make_int4(-1, 0, 0, 0), pm = make_int4(1, static_cast<int>(chunk), 0, 0);
+      const long long from = min(p0, total);
+      int4 pl = make_int4(-1, 0, 0, 0), pm = make_int4(1, static_cast<int>(from & 0xFFFFFFFF), static_cast<int>(from >> 32), 0);
       if (cap > 0) {   // where the piece begins: sequence, row, head, tiles of the unit before it; its tiles
         const KvSeq s = kv_seq<C::RB>(a, b_at);
         const int unit = static_cast<int>(off / s.tiles);
@@ -616,16 +624,29 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const KvAttnArgs a, con
   const KvJoin j = i0 < few.blocks - 1 ? few : many;
   const int c = (i0 < few.blocks - 1 ? i0 : i0 - max(0, few.blocks - 1)) + 1;
   const int4 pl = j.plan[2 * c], pm = j.plan[2 * c + 1];
-  const int z = pl.w, tiles = pm.x, chunk = pm.y;
-  if (pl.x < 0 || z == 0 || z > chunk) return;   // no piece; at a unit's start; a later piece of the unit
+  const int z = pl.w, tiles = pm.x;
+  if (pl.x < 0 || z == 0) return;   // no piece, or one that begins with a unit
+  // the unit's tiles [u0, u1) of the line; pieces c - 1, c, ... begin at from(c - 1), ...
+  auto from = [&](int i) {
+    const int4 m = j.plan[2 * i + 1];
+    return (static_cast<long long>(m.z) << 32) | static_cast<unsigned>(m.y);
+  };
+  const long long u0 = from(c) - z, u1 = u0 + tiles, f0 = from(c - 1);
+  if (f0 > u0) return;              // a later piece of the unit
   int begin, end, len;
   kv_rows(a.c, pl.x, begin, end, len);
   const int rows = (end - begin) * a.G - pl.y;
   const int RB = j.rows;
-  // pieces c - 1 (its last segment: the second slot unless the unit starts the piece), c, c + 1, ...
-  const int pieces = 1 + (tiles - z + chunk - 1) / chunk;
+  int pieces = 1;
+  for (int i = c; i < j.blocks; i += 32) {   // 32 pieces looked at in a step
+    const int l = i + static_cast<int>(threadIdx.x & 31);
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, l < j.blocks && from(l) < u1));
+    pieces += n;
+    if (n < 32) break;
+  }
+  // their results: of piece c - 1 its last segment (the second slot unless it begins with the unit), of the others the first
   const long long slot = static_cast<long long>(RB) * (D + 2);
-  const float* first = j.part + (2LL * (c - 1) + (z == chunk ? 0 : 1)) * slot;
+  const float* first = j.part + (2LL * (c - 1) + (f0 == u0 ? 0 : 1)) * slot;
   const float* rest = j.part + 2LL * c * slot;
   for (int at = blockIdx.y * 128 + threadIdx.x; at < RB * (D / 4); at += gridDim.y * 128) {
     const int row = at % RB, d0 = at / RB * 4;

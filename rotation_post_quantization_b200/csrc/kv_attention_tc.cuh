@@ -11,9 +11,9 @@
 //   warps 8-11, 12-15 queries of tile 0 and K / of tile 1 and V from a ring of
 //                    8 KB slots to fp16 operand tiles (128-byte swizzle; two of
 //                    K, three of V);
-//   warp 16          one thread issues S = Q K^T (both from shared memory) and
-//                    O += P V (P from tensor memory, V with its dims
-//                    contiguous, i.e. N-major);
+//   warps 16, 18     one thread each issues a tile's S = Q K^T (both from
+//                    shared memory) and O += P V (P from tensor memory, V with
+//                    its dims contiguous, i.e. N-major);
 //   warp 17          fills the ring: looks up page ids and scales of eight
 //                    steps at a time, copies pages and queries with tensor
 //                    copies (queries with asynchronous ones where a slot's rows
@@ -28,13 +28,11 @@
 // rare after the first steps and is done by the row's own thread.
 //
 // Tensor memory: S0, S1 (64 columns each), P0, P1 (2 x 32 each), O0, O1 (D
-// each). Shared memory at D = 128: Q 64 KB, K 32 KB, V 48 KB, ring 48 KB.
+// each). Shared memory at D = 128: Q 64 KB, K 32 KB, V 48 KB, ring 64 KB.
 //
 // Work: as in kv_attention.cuh one line of steps cut into equal pieces, here
 // with each row group's own number of steps (causal rows see fewer).
 #pragma once
-
-#include <type_traits>
 
 #include "kv_attention.cuh"
 
@@ -45,13 +43,17 @@ constexpr int kTcaGroup = 256;      // rows of a block
 constexpr int kTcaTile = 64;        // tokens of a step
 constexpr int kTcaThreads = 20 * 32;
 // registers of a thread of the rows', the operands' and the last warps:
-// 2 * 120 + 2 * 72 + 96 = 5 * 96, what 640 threads are launched with
-constexpr int kTcaRegsRows = 120, kTcaRegsCodes = 72, kTcaRegsLast = 96;
+// 2 * 144 + 2 * 56 + 80 = 5 * 96, what 640 threads are launched with
+constexpr int kTcaRegsRows = 144, kTcaRegsCodes = 56, kTcaRegsLast = 80;
 constexpr int kTcaVStages = 3;
 constexpr int kTcaMinTiles = 8;     // least piece of a block
+// A unit's queries, first step and output cost about as much as three steps;
+// the line of work counts them, so that blocks of many short units (a causal
+// prompt's first rows) get fewer of their steps.
+constexpr int kTcaUnitCost = 3;
 constexpr int kTcaMaxBlocks = 160;  // one per SM
-constexpr int kTcaMeta = 16;        // steps whose scales are kept (the ring is at most seven ahead of the rows)
-constexpr int kTcaSlots = 6;        // of the ring
+constexpr int kTcaMeta = 16;        // steps whose scales are kept (the ring is at most eight ahead of the rows)
+constexpr int kTcaSlots = 8;        // of the ring
 constexpr int kTcaSlot = 8192;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
@@ -174,8 +176,8 @@ __device__ __forceinline__ TcaSeq tca_seq(const KvAttnArgs& a, int b) {
 
 // First step and number of steps (at least 1) of row group g.
 __device__ __forceinline__ int2 tca_steps(const KvAttnArgs& a, int n, int len, int rows, int g) {
-  const int first = len - n + g * kTcaGroup / a.G;
-  const int last = len - n + (min(rows, (g + 1) * kTcaGroup) - 1) / a.G;
+  const int first = len - n + kv_div_g(a, g * kTcaGroup);
+  const int last = len - n + kv_div_g(a, min(rows, (g + 1) * kTcaGroup) - 1);
   const int hi = a.causal ? min(last, len - 1) : len - 1;
   if (hi < 0) return make_int2(0, 1);
   const int lo = a.window > 0 ? min(hi, max(0, first - a.window + 1)) : 0;
@@ -215,65 +217,85 @@ struct TcaCursor {
   }
 };
 
+// Position p of the line (each unit: kTcaUnitCost, then its steps): the unit
+// it falls in, the steps of that unit before it, and of the whole line.
+struct TcaPlace {
+  int b, g, h, z, tiles;
+  long long before;
+};
+
 // The block's piece: every lane of one warp.
 __device__ __forceinline__ void tca_locate(const KvAttnArgs& a, volatile int* sh) {
   const int lane = threadIdx.x & 31;
-  long long total = 0, p0 = 0, before = 0, chunk = 0;
-  int at_b = -1, at_g = 0, at_h = 0, at_z = 0, at_tiles = 0;
-  for (int pass = 0; pass < 2 && at_b < 0; ++pass) {
-    for (int b0 = 0; b0 < a.c.B && at_b < 0; b0 += 32) {
+  long long total = 0, steps = 0, chunk = 0, p[2] = {0, 0};
+  TcaPlace at[2] = {{-1, 0, 0, 0, 0, 0}, {-1, 0, 0, 0, 0, 0}};   // where this piece and the next one begin
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0, sbefore = 0;
+    for (int b0 = 0; b0 < a.c.B && at[1].b < 0; b0 += 32) {
       TcaSeq mine{0, 0, 0, 0, 0};
       if (b0 + lane < a.c.B) mine = tca_seq(a, b0 + lane);
       unsigned some = __ballot_sync(0xFFFFFFFFu, mine.groups > 0);
-      while (some && at_b < 0) {
+      while (some && at[1].b < 0) {
         const int f = __ffs(some) - 1;
         some &= some - 1;
         const int n = __shfl_sync(0xFFFFFFFFu, mine.n, f), len = __shfl_sync(0xFFFFFFFFu, mine.len, f);
         const int rows = __shfl_sync(0xFFFFFFFFu, mine.rows, f), groups = __shfl_sync(0xFFFFFFFFu, mine.groups, f);
-        for (int g0 = 0; g0 < groups; g0 += 32) {
+        for (int g0 = 0; g0 < groups && at[1].b < 0; g0 += 32) {
           const int tiles = g0 + lane < groups ? tca_steps(a, n, len, rows, g0 + lane).y : 0;
-          long long incl = static_cast<long long>(tiles) * a.c.H;
+          const int cost = tiles > 0 ? tiles + kTcaUnitCost : 0;
+          long long incl = static_cast<long long>(cost) * a.c.H, sincl = static_cast<long long>(tiles) * a.c.H;
           if (pass == 0) {
             total += incl;
+            steps += sincl;
             continue;
           }
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += t;
+            const long long t = __shfl_up_sync(0xFFFFFFFFu, incl, o), u = __shfl_up_sync(0xFFFFFFFFu, sincl, o);
+            if (lane >= o) {
+              incl += t;
+              sincl += u;
+            }
           }
-          const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > p0);
-          if (hit) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > p[e]);
+            if (at[e].b >= 0 || !hit) continue;
             const int l = __ffs(hit) - 1;
-            at_tiles = __shfl_sync(0xFFFFFFFFu, tiles, l);
-            const long long off =
-                p0 - before - __shfl_sync(0xFFFFFFFFu, incl - static_cast<long long>(tiles) * a.c.H, l);
-            at_b = b0 + f;
-            at_g = g0 + l;
-            at_h = static_cast<int>(off / at_tiles);
-            at_z = static_cast<int>(off % at_tiles);
-            break;
+            const int lt = __shfl_sync(0xFFFFFFFFu, tiles, l);
+            const long long off = p[e] - before - __shfl_sync(0xFFFFFFFFu, incl - static_cast<long long>(cost) * a.c.H, l);
+            const int h = static_cast<int>(off / (lt + kTcaUnitCost));
+            const int z = max(0, static_cast<int>(off - static_cast<long long>(h) * (lt + kTcaUnitCost)) - kTcaUnitCost);
+            at[e] = {b0 + f, g0 + l, h, z, lt,
+                     sbefore + __shfl_sync(0xFFFFFFFFu, sincl - static_cast<long long>(tiles) * a.c.H, l) +
+                         static_cast<long long>(h) * lt + z};
           }
           before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+          sbefore += __shfl_sync(0xFFFFFFFFu, sincl, 31);
         }
       }
     }
     if (pass == 0) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+      for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+        steps += __shfl_xor_sync(0xFFFFFFFFu, steps, o);
+      }
       chunk = max(static_cast<long long>(kTcaMinTiles), (total + gridDim.x - 1) / gridDim.x);
-      p0 = chunk * blockIdx.x;
-      if (p0 >= total) break;
+      p[0] = chunk * blockIdx.x;
+      p[1] = p[0] + chunk;
+      if (p[0] >= total) break;
     }
   }
   if (lane == 0) {
-    sh[0] = at_b;
-    sh[1] = at_g;
-    sh[2] = at_h;
-    sh[3] = at_z;
-    sh[4] = at_b < 0 ? 0 : static_cast<int>(min(chunk, total - p0));
-    a.plan[2 * blockIdx.x] = make_int4(at_b, at_g * kTcaGroup, at_h, at_z);
-    a.plan[2 * blockIdx.x + 1] = make_int4(at_tiles, static_cast<int>(chunk), 0, 0);
+    const long long first = at[0].b < 0 ? steps : at[0].before, end = at[1].b < 0 ? steps : at[1].before;
+    sh[0] = at[0].b;
+    sh[1] = at[0].g;
+    sh[2] = at[0].h;
+    sh[3] = at[0].z;
+    sh[4] = static_cast<int>(end - first);
+    a.plan[2 * blockIdx.x] = make_int4(at[0].b, at[0].g * kTcaGroup, at[0].h, at[0].z);
+    a.plan[2 * blockIdx.x + 1] = make_int4(at[0].tiles, static_cast<int>(first & 0xFFFFFFFF), static_cast<int>(first >> 32), 0);
   }
 }
 
@@ -316,7 +338,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(kfull + 8 * i, 4);
-      mbar_init(kempty + 8 * i, 1);
+      mbar_init(kempty + 8 * i, 2);   // both tiles' products
       mbar_init(qfull + 8 * i, 4);
       mbar_init(qempty + 8 * i, 1);
       mbar_init(sfull + 8 * i, 2);   // the product, and the issuing thread (it saw the step's scales)
@@ -328,13 +350,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     for (int i = 0; i < kTcaVStages; ++i) {
       mbar_init(vfull + 8 * i, 4);
-      mbar_init(vempty + 8 * i, 1);
+      mbar_init(vempty + 8 * i, 2);
     }
     for (int i = 0; i < kTcaSlots; ++i) {
       mbar_init(efull + 8 * i, 32);   // every lane of warp 17, and the bytes of its tensor copies
       mbar_init(eempty + 8 * i, 4);
     }
-    mbar_init(drained, 1);
+    mbar_init(drained, 2);
     fence_mbarrier_init();
   }
   if (warp == 16) {
@@ -377,12 +399,14 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int row = row0 + tile * kTcaRows + r;
         const bool live = row < cur.s.rows;
         const int rr = min(row, cur.s.rows - 1);
-        const int tok = rr / a.G, hq = cur.h * a.G + rr % a.G;
+        const int tok = kv_div_g(a, rr), hq = cur.h * a.G + rr - tok * a.G;
         const int pos = cur.s.len - cur.s.n + tok;
         const int hi = a.causal ? min(pos, cur.s.len - 1) : cur.s.len - 1;
         const int lo = a.window > 0 ? pos - a.window + 1 : 0;
         float M = -INFINITY, l = 0.0f, coef = 0.0f;
         for (int j = 0; j < n; ++j, ++use) {
+          // S of this step also says that P's place is free: its arrival follows every product that
+          // its thread issued before, PV of use - 2 among them.
           ok = mbar_wait_warp(sfull + 8 * tile, use & 1, kSiteKvAccum);
           if (!ok) break;
           tc_fence_after();
@@ -408,71 +432,76 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
               for (int i = 0; i < 32; ++i)
                 if (32 * c + i < first || 32 * c + i > last) v[c][i] = 0xFF800000u;   // -inf
           }
-          // ---- maximum of the exponents: of each 16 tokens' products, then with their scales. A
-          // factor of 0 (all products are 0, or are to count as 0) becomes one that keeps -inf.
-          float mx = -INFINITY;
-          float ck[4], of[4], iv[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const KvScale sc = meta[c];
-            const uint32_t* x = &v[c / 2][16 * (c % 2)];
-            float m[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              m[i] = fmaxf(fmaxf(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
-                           fmaxf(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
-            const float m4 = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-            ck[c] = fmaxf(coef * sc.k, 1e-37f);
-            of[c] = sc.lv;
-            iv[c] = sc.iv;
-            mx = fmaxf(mx, fmaf(m4, ck[c], sc.lv));
-          }
-          if (__any_sync(0xFFFFFFFFu, mx > M + (kKvBias + kKvLazy))) {
-            const float Mn = mx > M + (kKvBias + kKvLazy) ? mx - kKvBias : M;
-            const float f = Mn == M ? 1.0f : ex2(M - Mn);   // 0 from nothing
-            M = Mn;
-            l *= f;
-            if (j > 0) {
-              ok = product(use - 1);
-              if (!ok) break;
-              tc_fence_after();
+          // ---- weights against the maximum of the steps before, their sum and their own maximum: the
+          // comparisons run beside the exponentials. Where an exponent passes M by 2^14 (the unit's
+          // first step, and rarely later) the maximum moves and the weights are formed again. A factor
+          // of 0 (all products are 0, or are to count as 0) becomes one that keeps -inf.
+          uint32_t p[2][16];
+          float ls = 0.0f;
 #pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t u[16];
-                tmem_ld_32x32b_x16(to + 16 * c, u);
-                tmem_wait_ld();
+          for (bool again = j == 0;;) {
+            float mx = -INFINITY;
+            if (again) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
-                tmem_st_32x32b_x16(to + 16 * c, u);
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t* x = &v[c / 2][16 * (c % 2)];
+                float m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  m[i] = fmaxf(fmaxf(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
+                               fmaxf(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
+                mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(coef * meta[c].k, 1e-37f), meta[c].lv));
+              }
+              const float Mn = mx > M + (kKvBias + kKvLazy) ? mx - kKvBias : M;
+              const float f = Mn == M ? 1.0f : ex2(M - Mn);   // 0 from nothing
+              M = Mn;
+              l *= f;
+              if (j > 0) {
+                ok = product(use - 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t u[16];
+                  tmem_ld_32x32b_x16(to + 16 * c, u);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+                  tmem_st_32x32b_x16(to + 16 * c, u);
+                }
               }
             }
-          }
-          // ---- weights, their sum, and P
-          const float Ms = M == -INFINITY ? 0.0f : M;
-          if (use >= 2) ok = product(use - 2);
-          if (!ok) break;
-          tc_fence_after();
+            const float Ms = M == -INFINITY ? 0.0f : M;
+            ls = 0.0f;
+            mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t p[16];
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-              const float o = of[2 * c + hb] - Ms;
-              const uint64_t ck2 = f32x2(ck[2 * c + hb], ck[2 * c + hb]), of2 = f32x2(o, o);
+            for (int c = 0; c < 4; ++c) {
+              const KvScale sc = meta[c];
+              const float ck = fmaxf(coef * sc.k, 1e-37f), o = sc.lv - Ms;
+              const uint64_t ck2 = f32x2(ck, ck), of2 = f32x2(o, o);
               uint64_t sum[2] = {0, 0};
+              float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
               for (int i = 0; i < 16; i += 2) {
                 const float2 e = f32x2_split(fma_f32x2(
-                    f32x2(__uint_as_float(v[c][16 * hb + i]), __uint_as_float(v[c][16 * hb + i + 1])), ck2, of2));
+                    f32x2(__uint_as_float(v[c / 2][16 * (c % 2) + i]), __uint_as_float(v[c / 2][16 * (c % 2) + i + 1])), ck2, of2));
                 const float x = ex2(e.x), y = ex2(e.y);
+                m[(i / 2) & 1] = fmaxf(m[(i / 2) & 1], fmaxf(e.x, e.y));
                 sum[(i / 2) & 1] = add_f32x2(sum[(i / 2) & 1], f32x2(x, y));
-                p[8 * hb + i / 2] = pack_f16x2(x, y);
+                p[c / 2][8 * (c % 2) + i / 2] = pack_f16x2(x, y);
               }
+              mx = fmaxf(mx, fmaxf(m[0], m[1]));
               const float2 s2 = f32x2_split(add_f32x2(sum[0], sum[1]));
-              l = fmaf(s2.x + s2.y, iv[2 * c + hb], l);
+              ls = fmaf(s2.x + s2.y, sc.iv, ls);
             }
-            tmem_st_32x32b_x16(tp + 32 * (use & 1) + 16 * c, p);
+            // (after the maximum has moved no exponent passes it; before anything was seen M counts as 0)
+            again = !again && __any_sync(0xFFFFFFFFu, mx > kKvBias + kKvLazy || (M == -INFINITY && mx > -INFINITY));
+            if (!again) break;
           }
+          if (!ok) break;
+          l += ls;
+          tmem_st_32x32b_x16(tp + 32 * (use & 1), p[0]);
+          tmem_st_32x32b_x16(tp + 32 * (use & 1) + 16, p[1]);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
@@ -598,10 +627,12 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           for (int i = 0; i < RE * L / 128; ++i) {
             const int r = r0 + pt / L + 128 / L * i;
             const uint4 w = reinterpret_cast<const uint4*>(from)[pt + 128 * i];
-            uint32_t m = bf16x8_finite_amax(w);
+            // (a row with an infinity or NaN is scaled as one of 2^127: its results are not finite anyway)
+            uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+            m = max(m & 0xFFFFu, m >> 16);
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const int e = max(-110, static_cast<int>(m >> 7) - 127);
+            const int e = max(-110, min(127, static_cast<int>(m >> 7) - 127));
             // a negative scale goes with the queries, so that the factors are not negative
             const float up = copysignf(__int_as_float((14 - e + 127) << 23), a.scale);
             float f[8];
@@ -699,13 +730,13 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
               if (RE % a.G == 0) {   // whole tokens: rows behind the sequence are anybody's, and dead
                 if (lane == 0) {
                   mbar_arrive_expect_tx(efull + 8 * slot, kTcaSlot);
-                  tma_load_3d(dst, &tmQ, 0, cur.h * a.G, cur.s.begin + row0 / a.G, efull + 8 * slot);
+                  tma_load_3d(dst, &tmQ, 0, cur.h * a.G, cur.s.begin + kv_div_g(a, row0), efull + 8 * slot);
                 } else {
                   mbar_arrive(efull + 8 * slot);
                 }
               } else {
-                int tok = (row0 + lane / L) / a.G, g = (row0 + lane / L) % a.G;
-                const int dt = (32 / L) / a.G, dg = (32 / L) % a.G;
+                int tok = kv_div_g(a, row0 + lane / L), g = row0 + lane / L - tok * a.G;
+                const int dt = kv_div_g(a, 32 / L), dg = 32 / L - dt * a.G;
 #pragma unroll 1
                 for (int i = 0; i < RE * L / 32; ++i) {
                   const bool in = tok < cur.s.n;
@@ -747,35 +778,29 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       // leave only once the last copies have landed, whatever became of the others
       for (int i = max(0, used - kTcaSlots); i < used; ++i)
         mbar_wait(efull + 8 * (i % kTcaSlots), (i / kTcaSlots) & 1, kSiteKvLoad);
-    } else if (warp == 16 && elect_one()) {
-      // ---------------------------------------------- tensor core
+    } else if ((warp == 16 || warp == 18) && elect_one()) {
+      // ---------------------------------------------- tensor core, one thread a tile
       constexpr uint32_t is = umma_idesc_f16(kTcaRows, kTcaTile, false), io = umma_idesc_f16(kTcaRows, D, true);
-      // This thread's own time bounds the kernel where it is long (24 products
-      // and 6 commits a step), so what a step needs is kept in a few scalars.
+      const int tile = (warp - 16) >> 1;
+      const uint32_t ts = tmem + tile * 64, tp = tmem + 128 + tile * 64, to = tmem + 256 + tile * D;
+      const uint64_t dq = umma_desc_sw128(base + C::OQ) + tile * (C::OpQ >> 4);   // addresses in 16 bytes
+      const uint64_t dk = umma_desc_sw128(base + C::OK), dv = umma_desc_sw128_n(base + C::OV, Block);
       bool ok = true;
-      uint32_t ph_q0 = 0, ph_q1 = 0;                     // units of the tiles
-      uint32_t s0 = 0, s1 = 0, p0 = 0, p1 = 0;           // scores and products of the tiles issued
-      struct At {
-        int step, tiles;      // step of the piece; tiles it has (0: none)
-        bool first, last;     // of its unit
-      };
-      int j = 0, n = cur.steps();
-      auto tiles_of = [&]() { return cur.g * kTcaGroup + kTcaRows < cur.s.rows ? 2 : 1; };
-      const uint64_t dq = umma_desc_sw128(base + C::OQ), dk = umma_desc_sw128(base + C::OK);   // addresses in 16 bytes
-      const uint64_t dv = umma_desc_sw128_n(base + C::OV, Block);
-      auto scores = [&](auto tile, const At& x) {
-        constexpr int t = decltype(tile)::value;
-        if (!ok || t >= x.tiles) return;
-        uint32_t& done = t ? s1 : s0;
-        const int st = x.step & 1;
-        if (t == 0) ok = mbar_wait(kfull + 8 * st, (x.step >> 1) & 1, kSiteKvLoad);
-        if (x.first) {
-          uint32_t& ph = t ? ph_q1 : ph_q0;
-          ok = ok && mbar_wait(qfull + 8 * t, ph, kSiteKvLoad);
-          ph ^= 1;
+      uint32_t units = 0, scored = 0, used = 0;   // of this tile: units, S and PV issued
+      // S of a step (of the piece; the unit's first or last)
+      auto scores = [&](int step, bool mine, bool first, bool last) {
+        const int st = step & 1;
+        ok = mbar_wait(kfull + 8 * st, (step >> 1) & 1, kSiteKvLoad);
+        if (!mine) {   // a unit without this tile: only K's stage is passed on
+          if (ok) mbar_arrive(kempty + 8 * st);
+          return;
         }
-        if (done > 0) ok = ok && mbar_wait(sfree + 8 * t, (done - 1) & 1, kSiteKvAccum);   // the last S is read
-        ++done;
+        if (first) {
+          ok = ok && mbar_wait(qfull + 8 * tile, units & 1, kSiteKvLoad);
+          ++units;
+        }
+        if (scored > 0) ok = ok && mbar_wait(sfree + 8 * tile, (scored - 1) & 1, kSiteKvAccum);   // the last S is read
+        ++scored;
         if (!ok) return;
         tc_fence_after();
         const uint64_t dks = dk + st * (C::Op >> 4);
@@ -783,51 +808,47 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_bf16(tmem + t * 64, dq + t * (C::OpQ >> 4) + kb * (BlockQ >> 4) + 2 * k,
-                        dks + kb * (Block >> 4) + 2 * k, is, kb + k > 0);
-        mbar_arrive(sfull + 8 * t);
-        tc_commit(sfull + 8 * t);
-        if (x.last) tc_commit(qempty + 8 * t);
-        if (t == x.tiles - 1) tc_commit(kempty + 8 * st);
+            tc_mma_bf16(ts, dq + kb * (BlockQ >> 4) + 2 * k, dks + kb * (Block >> 4) + 2 * k, is, kb + k > 0);
+        mbar_arrive(sfull + 8 * tile);
+        tc_commit(sfull + 8 * tile);
+        tc_commit(kempty + 8 * st);
+        if (last) tc_commit(qempty + 8 * tile);
       };
-      auto product = [&](auto tile, const At& x) {
-        constexpr int t = decltype(tile)::value;
-        if (!ok || t >= x.tiles) return;
-        const uint32_t use = t ? p1++ : p0++;
-        const int st = x.step % kTcaVStages, pb = use & 1;
-        if (t == 0) ok = mbar_wait(vfull + 8 * st, (x.step / kTcaVStages) & 1, kSiteKvLoad);
-        ok = ok && mbar_wait(pfull + 16 * t + 8 * pb, (use >> 1) & 1, kSiteKvAccum);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t dvs = dv + st * (C::Op >> 4);
-#pragma unroll
-        for (int k = 0; k < kTcaTile / 16; ++k)
-          tc_mma_f16_ta(tmem + 256 + t * D, tmem + 128 + t * 64 + 32 * pb + 8 * k, dvs + 128 * k, io, !x.first || k > 0);
-        tc_commit(pfree + 16 * t + 8 * pb);
-        if (t == x.tiles - 1) tc_commit(vempty + 8 * st);
-      };
-      const std::integral_constant<int, 0> t0{};
-      const std::integral_constant<int, 1> t1{};
-      // In time: the tiles run half a step apart.
-      At before{-1, 0, false, false}, now{0, cur.left > 0 ? tiles_of() : 0, true, n == 1};
-      scores(t0, now);
-      scores(t1, now);
-      while (ok && (now.tiles > 0 || before.tiles > 0)) {
-        At next{now.step + 1, now.tiles, false, false};
-        if (now.tiles > 0 && ++j == n) {   // the next unit's first step
+      auto is_mine = [&]() { return cur.g * kTcaGroup + tile * kTcaRows < cur.s.rows; };
+      int j = 0, n = cur.left > 0 ? cur.steps() : 0, vst = 0, ph_v = 0;
+      bool mine = cur.left > 0 && is_mine();
+      if (cur.left > 0) scores(0, mine, true, n == 1);
+      for (int step = 0; cur.left > 0 && ok; ++step) {
+        const bool now = mine, first = j == 0;
+        if (++j == n) {   // the next step is the next unit's first
           cur.next(a);
           j = 0;
-          n = cur.steps();
-          next.tiles = cur.left > 0 ? tiles_of() : 0;
-          next.first = true;
+          if (cur.left > 0) {
+            n = cur.steps();
+            mine = is_mine();
+          }
         }
-        next.last = j == n - 1;
-        scores(t0, next);
-        product(t1, before);
-        scores(t1, next);
-        product(t0, now);
-        before = now;
-        now = next;
+        if (cur.left > 0) scores(step + 1, mine, j == 0, j == n - 1);
+        ok = ok && mbar_wait(vfull + 8 * vst, ph_v, kSiteKvLoad);
+        if (now) {
+          const int pb = used & 1;
+          ok = ok && mbar_wait(pfull + 16 * tile + 8 * pb, (used >> 1) & 1, kSiteKvAccum);
+          if (!ok) break;
+          ++used;
+          tc_fence_after();
+          const uint64_t dvs = dv + vst * (C::Op >> 4);
+#pragma unroll
+          for (int k = 0; k < kTcaTile / 16; ++k)
+            tc_mma_f16_ta(to, tp + 32 * pb + 8 * k, dvs + 128 * k, io, !first || k > 0);
+          tc_commit(pfree + 16 * tile + 8 * pb);
+          tc_commit(vempty + 8 * vst);
+        } else if (ok) {
+          mbar_arrive(vempty + 8 * vst);
+        }
+        if (++vst == kTcaVStages) {
+          vst = 0;
+          ph_v ^= 1;
+        }
       }
       // nothing issued here may still run when the tensor memory is given back
       tc_commit(drained);
