@@ -104,6 +104,25 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Whether the phase has completed, without suspending the thread.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One arrival of a converged warp, without a branch.
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
 template <int R>
 __device__ __forceinline__ void regs_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -403,11 +422,16 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int pos = cur.s.len - cur.s.n + tok;
         const int hi = a.causal ? min(pos, cur.s.len - 1) : cur.s.len - 1;
         const int lo = a.window > 0 ? pos - a.window + 1 : 0;
+        // steps in which no row of the warp has a masked token: [whole0, whole1)
+        const int first_t = (cur.t0 + cur.z) * kTcaTile;
+        const int whole0 = (max(0, __reduce_max_sync(0xFFFFFFFFu, lo) - first_t) + kTcaTile - 1) / kTcaTile;
+        const int whole1 = (__reduce_min_sync(0xFFFFFFFFu, hi) + 1 - first_t) / kTcaTile;   // (below 0: none)
         float M = -INFINITY, l = 0.0f, coef = 0.0f;
+        bool there = false;   // S of the step has been seen complete
         for (int j = 0; j < n; ++j, ++use) {
           // S of this step also says that P's place is free: its arrival follows every product that
           // its thread issued before, PV of use - 2 among them.
-          ok = mbar_wait_warp(sfull + 8 * tile, use & 1, kSiteKvAccum);
+          if (!there) ok = mbar_wait_warp(sfull + 8 * tile, use & 1, kSiteKvAccum);
           if (!ok) break;
           tc_fence_after();
           uint32_t v[2][32];
@@ -416,14 +440,22 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (j == 0) coef = reinterpret_cast<const float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r];
           const int t = (cur.t0 + cur.z + j) * kTcaTile;
           const KvScale* meta = reinterpret_cast<const KvScale*>(smem + C::OMeta) + ((step + j) % kTcaMeta) * 4;
-          const bool whole = __all_sync(0xFFFFFFFFu, t >= lo && t + kTcaTile - 1 <= hi);
+          const bool whole = j >= whole0 && j < whole1;
+          const bool unseen = M == -INFINITY && t <= hi && t + kTcaTile - 1 >= lo;   // the row's first tokens
+          // a factor of 0 (all products are 0, or are to count as 0) becomes one that keeps -inf
+          float ck[4], lv[4], iv[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const KvScale sc = meta[c];
+            ck[c] = fmaxf(coef * sc.k, 1e-37f);
+            lv[c] = sc.lv;
+            iv[c] = sc.iv;
+          }
           tmem_wait_ld();
           tmem_values(v[0]);
           tmem_values(v[1]);
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sfree + 8 * tile);
-          __syncwarp();
+          mbar_arrive_warp(sfree + 8 * tile);   // (the wait for the loads is the whole warp's)
           if (!whole) {
             const int first = lo - t, last = hi - t;
 #pragma unroll
@@ -434,14 +466,12 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           }
           // ---- weights against the maximum of the steps before, their sum and their own maximum: the
           // comparisons run beside the exponentials. Where an exponent passes M by 2^14 (the unit's
-          // first step, and rarely later) the maximum moves and the weights are formed again. A factor
-          // of 0 (all products are 0, or are to count as 0) becomes one that keeps -inf.
-          uint32_t p[2][16];
+          // first step, and rarely later) the maximum moves and the weights are formed again.
           float ls = 0.0f;
 #pragma unroll 1
           for (bool again = j == 0;;) {
-            float mx = -INFINITY;
             if (again) {
+              float mx = -INFINITY;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const uint32_t* x = &v[c / 2][16 * (c % 2)];
@@ -450,7 +480,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int i = 0; i < 4; ++i)
                   m[i] = fmaxf(fmaxf(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
                                fmaxf(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
-                mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), fmaxf(coef * meta[c].k, 1e-37f), meta[c].lv));
+                mx = fmaxf(mx, fmaf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), ck[c], lv[c]));
               }
               const float Mn = mx > M + (kKvBias + kKvLazy) ? mx - kKvBias : M;
               const float f = Mn == M ? 1.0f : ex2(M - Mn);   // 0 from nothing
@@ -473,40 +503,44 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             const float Ms = M == -INFINITY ? 0.0f : M;
             ls = 0.0f;
-            mx = -INFINITY;
+            __half2 top[2] = {__half2half2(__ushort_as_half(0)), __half2half2(__ushort_as_half(0))};
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const KvScale sc = meta[c];
-              const float ck = fmaxf(coef * sc.k, 1e-37f), o = sc.lv - Ms;
-              const uint64_t ck2 = f32x2(ck, ck), of2 = f32x2(o, o);
-              uint64_t sum[2] = {0, 0};
-              float m[2] = {-INFINITY, -INFINITY};
+            for (int c = 0; c < 2; ++c) {
+              uint32_t p[16];
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                const float2 e = f32x2_split(fma_f32x2(
-                    f32x2(__uint_as_float(v[c / 2][16 * (c % 2) + i]), __uint_as_float(v[c / 2][16 * (c % 2) + i + 1])), ck2, of2));
-                const float x = ex2(e.x), y = ex2(e.y);
-                m[(i / 2) & 1] = fmaxf(m[(i / 2) & 1], fmaxf(e.x, e.y));
-                sum[(i / 2) & 1] = add_f32x2(sum[(i / 2) & 1], f32x2(x, y));
-                p[c / 2][8 * (c % 2) + i / 2] = pack_f16x2(x, y);
+              for (int hb = 0; hb < 2; ++hb) {
+                const float o = lv[2 * c + hb] - Ms;
+                const uint64_t ck2 = f32x2(ck[2 * c + hb], ck[2 * c + hb]), of2 = f32x2(o, o);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                  const float2 e = f32x2_split(fma_f32x2(
+                      f32x2(__uint_as_float(v[c][16 * hb + i]), __uint_as_float(v[c][16 * hb + i + 1])), ck2, of2));
+                  const float x = ex2(e.x), y = ex2(e.y);
+                  const uint32_t w = pack_f16x2(x, y);
+                  p[8 * hb + i / 2] = w;
+                  sum[(i / 2) & 1] = add_f32x2(sum[(i / 2) & 1], f32x2(x, y));
+                  top[(i / 2) & 1] = __hmax2(top[(i / 2) & 1], *reinterpret_cast<const __half2*>(&w));
+                }
+                const float2 s2 = f32x2_split(add_f32x2(sum[0], sum[1]));
+                ls = fmaf(s2.x + s2.y, iv[2 * c + hb], ls);
               }
-              mx = fmaxf(mx, fmaxf(m[0], m[1]));
-              const float2 s2 = f32x2_split(add_f32x2(sum[0], sum[1]));
-              ls = fmaf(s2.x + s2.y, sc.iv, ls);
+              tmem_st_32x32b_x16(tp + 32 * (use & 1) + 16 * c, p);
+              // the next step's S, looked at where the answer is not waited for
+              if (c == 0) there = j + 1 < n && mbar_test_wait(sfull + 8 * tile, (use + 1) & 1);
             }
-            // (after the maximum has moved no exponent passes it; before anything was seen M counts as 0)
-            again = !again && __any_sync(0xFFFFFFFFu, mx > kKvBias + kKvLazy || (M == -INFINITY && mx > -INFINITY));
+            // (after the maximum has moved no weight passes 2^14)
+            const __half2 tt = __hmax2(top[0], top[1]);
+            const float limit = 16384.0f;   // 2^(kKvBias + kKvLazy)
+            there = __all_sync(0xFFFFFFFFu, there);
+            again = !again && __any_sync(0xFFFFFFFFu, unseen || __low2float(tt) > limit || __high2float(tt) > limit);
             if (!again) break;
           }
           if (!ok) break;
           l += ls;
-          tmem_st_32x32b_x16(tp + 32 * (use & 1), p[0]);
-          tmem_st_32x32b_x16(tp + 32 * (use & 1) + 16, p[1]);
           tmem_wait_st();
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + 16 * tile + 8 * (use & 1));
-          __syncwarp();
+          mbar_arrive_warp(pfull + 16 * tile + 8 * (use & 1));
         }
         if (ok) ok = product(use - 1);
         if (!ok) break;
