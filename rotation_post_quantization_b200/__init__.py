@@ -237,30 +237,56 @@ def respin_quantize_rowmax(u, rowmax, q_packed, scale, flags: int = 0, stream=No
                                       _ptr(scale), ctypes.c_uint(flags), _stream(stream)))
 
 
-def _want(t, name, dtype, shape, like=None):
-    """Check a tensor's type, shape (None: any size) and device; the kernels
-    read what these say is there."""
+# The calls below check what the kernels rely on (a small call is as long as
+# its host part, so the checks are comparisons first and messages second).
+
+def _want(t, name, dtype, shape, dev):
+    """A tensor of this type and shape on this device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        return
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    s = t.shape
-    if len(s) != len(shape) or any(w is not None and w != g for w, g in zip(shape, s)):
-        raise ValueError(f"{name} must have shape {list(shape)}, not {list(s)}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, not {list(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _dense(**tensors):
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
 def _heads_ld(t, name):
     """Stride between tokens of [N, heads, head_dim] with contiguous heads."""
-    st, s = t.stride(), t.shape
-    if st[2] != 1 and s[2] > 1 or st[1] != s[2] and s[1] > 1:
-        raise ValueError(f"{name}: heads and head_dim must be contiguous (strides {list(st)})")
-    return st[0] if s[0] > 1 else max(8, s[1] * s[2])
+    a, b, c = t.stride()
+    n, h, d = t.shape
+    if (c != 1 and d > 1) or (b != d and h > 1):
+        raise ValueError(f"{name}: heads and head_dim must be contiguous (strides {[a, b, c]})")
+    return a if n > 1 else max(8, h * d)
 
 
 def _current_device(t, name):
     import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    return dev
+
+
+def _stream_on(stream, dev):
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the handle without a Stream object around it
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _3d(t, name):
+    s = t.shape
+    if len(s) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], not {list(s)}")
+    return s
 
 
 class KvCache(NamedTuple):
@@ -282,26 +308,32 @@ class KvCache(NamedTuple):
 
 
 def _kv_args(cache, N, kv_len, block_table, cu):
-    """(respin_kv_cache_t, respin_kv_batch_t) of checked tensors."""
+    """(respin_kv_cache_t, respin_kv_batch_t, device) of checked tensors."""
     import torch
     k, v, ks, vs = cache
-    _current_device(k, "cache.k")
-    _want(k, "cache.k", torch.int8, (None,) * 4)
-    pages, heads, page_size, d = k.shape
-    _want(v, "cache.v", torch.int8, k.shape, k)
-    _want(ks, "cache.k_scale", torch.float32, (pages, heads), k)
-    _want(vs, "cache.v_scale", torch.float32, (pages, heads), k)
-    B = kv_len.shape[0]
-    _want(kv_len, "kv_len", torch.int32, (B,), k)
-    _want(block_table, "block_table", torch.int32, (B, None), k)
+    dev = _current_device(k, "cache.k")
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"cache.k must be [num_pages, kv_heads, page_size, head_dim], not {list(shape)}")
+    pages, heads, page_size, d = shape
+    f32, i32 = torch.float32, torch.int32
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be [B, max_pages], not {list(block_table.shape)}")
+    B, max_pages = block_table.shape
+    _want(k, "cache.k", torch.int8, shape, dev)
+    _want(v, "cache.v", torch.int8, shape, dev)
+    _want(ks, "cache.k_scale", f32, (pages, heads), dev)
+    _want(vs, "cache.v_scale", f32, (pages, heads), dev)
+    _want(kv_len, "kv_len", i32, (B,), dev)
+    _want(block_table, "block_table", i32, (B, max_pages), dev)
     if cu is not None:
-        _want(cu, "cu", torch.int32, (B + 1,), k)
+        _want(cu, "cu", i32, (B + 1,), dev)
     if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
             and kv_len.is_contiguous() and block_table.is_contiguous() and (cu is None or cu.is_contiguous())):
         raise ValueError("the cache, kv_len, block_table and cu must be contiguous")
     return (_KvCacheC(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page_size, heads, d),
-            _KvBatchC(None if cu is None else cu.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
-                      B, block_table.shape[1], N))
+            _KvBatchC(None if cu is None else cu.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), B, max_pages, N),
+            dev)
 
 
 def respin_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None,
@@ -312,26 +344,26 @@ def respin_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, 
     fp32 [rot_dim / 2]."""
     import torch
     bf = torch.bfloat16
-    _current_device(q, "q")
-    _want(q, "q", bf, (None, None, None))
-    N, Hq, d = q.shape
-    _want(k, "k", bf, (N, None, d), q)
-    Hk = k.shape[1]
-    _want(q_out, "q_out", bf, q.shape, q)
-    _want(k_out, "k_out", bf, k.shape, q)
-    _want(positions, "positions", torch.int32, (N,), q)
-    _want(inv_freq, "inv_freq", torch.float32, (None,), q)
-    if not (positions.is_contiguous() and inv_freq.is_contiguous()):
-        raise ValueError("positions and inv_freq must be contiguous")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _want(w, name, bf, (d,), q)
-            if not w.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
+    dev = _current_device(q, "q")
+    N, Hq, d = _3d(q, "q")
+    Hk = _3d(k, "k")[1]
+    half = inv_freq.numel()
+    _want(q, "q", bf, (N, Hq, d), dev)
+    _want(k, "k", bf, (N, Hk, d), dev)
+    _want(q_out, "q_out", bf, (N, Hq, d), dev)
+    _want(k_out, "k_out", bf, (N, Hk, d), dev)
+    _want(positions, "positions", torch.int32, (N,), dev)
+    _want(inv_freq, "inv_freq", torch.float32, (half,), dev)
+    if q_weight is not None:
+        _want(q_weight, "q_weight", bf, (d,), dev)
+    if k_weight is not None:
+        _want(k_weight, "k_weight", bf, (d,), dev)
+    _dense(positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
     _check(lib.respin_qk_norm_rope(
         q.data_ptr(), k.data_ptr(), N, Hq, Hk, d, _heads_ld(q, "q"), _heads_ld(k, "k"), _ptr(q_weight),
-        _ptr(k_weight), eps, positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(interleaved),
-        q_out.data_ptr(), k_out.data_ptr(), _heads_ld(q_out, "q_out"), _heads_ld(k_out, "k_out"), _stream(stream)))
+        _ptr(k_weight), eps, positions.data_ptr(), inv_freq.data_ptr(), 2 * half, interleaved,
+        q_out.data_ptr(), k_out.data_ptr(), _heads_ld(q_out, "q_out"), _heads_ld(k_out, "k_out"),
+        _stream_on(stream, dev)))
 
 
 def respin_kv_append(cache: KvCache, k, v, kv_len, block_table, cu=None, stream=None) -> None:
@@ -341,11 +373,12 @@ def respin_kv_append(cache: KvCache, k, v, kv_len, block_table, cu=None, stream=
     (None: N / B each), block_table int32 [B, max_pages] names the pages."""
     import torch
     N = k.shape[0]
-    c, b = _kv_args(cache, N, kv_len, block_table, cu)
+    c, b, dev = _kv_args(cache, N, kv_len, block_table, cu)
     shape = (N, c.kv_heads, c.head_dim)
-    _want(k, "k", torch.bfloat16, shape, cache.k)
-    _want(v, "v", torch.bfloat16, shape, cache.k)
-    _check(lib.respin_kv_append(c, b, k.data_ptr(), v.data_ptr(), _heads_ld(k, "k"), _heads_ld(v, "v"), _stream(stream)))
+    _want(k, "k", torch.bfloat16, shape, dev)
+    _want(v, "v", torch.bfloat16, shape, dev)
+    _check(lib.respin_kv_append(c, b, k.data_ptr(), v.data_ptr(), _heads_ld(k, "k"), _heads_ld(v, "v"),
+                                _stream_on(stream, dev)))
 
 
 def respin_kv_read(cache: KvCache, k_out, v_out, kv_len, block_table, cu=None, stream=None) -> None:
@@ -353,12 +386,12 @@ def respin_kv_read(cache: KvCache, k_out, v_out, kv_len, block_table, cu=None, s
     [N, kv_heads, d]); kv_len, block_table and cu as in respin_kv_append."""
     import torch
     N = k_out.shape[0]
-    c, b = _kv_args(cache, N, kv_len, block_table, cu)
+    c, b, dev = _kv_args(cache, N, kv_len, block_table, cu)
     shape = (N, c.kv_heads, c.head_dim)
-    _want(k_out, "k_out", torch.bfloat16, shape, cache.k)
-    _want(v_out, "v_out", torch.bfloat16, shape, cache.k)
+    _want(k_out, "k_out", torch.bfloat16, shape, dev)
+    _want(v_out, "v_out", torch.bfloat16, shape, dev)
     _check(lib.respin_kv_read(c, b, k_out.data_ptr(), v_out.data_ptr(), _heads_ld(k_out, "k_out"),
-                              _heads_ld(v_out, "v_out"), _stream(stream)))
+                              _heads_ld(v_out, "v_out"), _stream_on(stream, dev)))
 
 
 def respin_kv_attention_workspace(cache: KvCache, q_heads: int, N: int, max_q=None) -> int:
@@ -378,24 +411,21 @@ def respin_kv_attention(cache: KvCache, q, kv_len, block_table, out, workspace, 
     respin_kv_attention_workspace bytes, one for each call that may run at the
     same time. kv_len, block_table and cu as in respin_kv_append."""
     import torch
-    N = q.shape[0]
-    c, b = _kv_args(cache, N, kv_len, block_table, cu)
-    k, d = cache.k, c.head_dim
-    _want(q, "q", torch.bfloat16, (N, None, d), k)
-    Hq = q.shape[1]
-    _want(out, "out", torch.bfloat16, (N, Hq, d), k)
-    _want(workspace, "workspace", torch.uint8, (None,), k)
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
+    bf = torch.bfloat16
+    N, Hq, _ = _3d(q, "q")
+    c, b, dev = _kv_args(cache, N, kv_len, block_table, cu)
+    d, size = c.head_dim, workspace.numel()
+    _want(q, "q", bf, (N, Hq, d), dev)
+    _want(out, "out", bf, (N, Hq, d), dev)
+    _want(workspace, "workspace", torch.uint8, (size,), dev)
     if lse is not None:
-        _want(lse, "lse", torch.float32, (N, Hq), k)
-        if not lse.is_contiguous():
-            raise ValueError("lse must be contiguous")
+        _want(lse, "lse", torch.float32, (N, Hq), dev)
+    _dense(workspace=workspace, lse=lse)
     if cu is None and b.B > 0:
         max_q = N // b.B
-    _check(lib.respin_kv_attention(c, b, q.data_ptr(), Hq, _heads_ld(q, "q"), max_q or 0, int(causal), int(window),
+    _check(lib.respin_kv_attention(c, b, q.data_ptr(), Hq, _heads_ld(q, "q"), max_q or 0, causal, window,
                                    d ** -0.5 if scale is None else scale, out.data_ptr(), _heads_ld(out, "out"),
-                                   _ptr(lse), workspace.data_ptr(), workspace.shape[0], _stream(stream)))
+                                   _ptr(lse), workspace.data_ptr(), size, _stream_on(stream, dev)))
 
 
 def _host_f32(a, shape, name):
