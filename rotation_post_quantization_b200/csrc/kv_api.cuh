@@ -233,13 +233,15 @@ respin_status_t respin_kv_append(const respin_kv_cache_t* cache, const respin_kv
   // step has a block for each sequence and a prefill one for each page.
   const int per = batch->N / batch->B;
   a.rows = per < 1 ? 1 : per > P ? P : per;
-  const int T = P * D > kKvScaleChunks * 8 * 128 ? 256 : 128;
-  const void* fn = D == 64 ? reinterpret_cast<const void*>(&kv_append_kernel<64, 128>)
-                 : T == 128 ? reinterpret_cast<const void*>(&kv_append_kernel<128, 128>)
-                            : reinterpret_cast<const void*>(&kv_append_kernel<128, 256>);
-  const dim3 grid(static_cast<unsigned>((batch->N + a.rows - 1) / a.rows), static_cast<unsigned>(cache->kv_heads), 2);
+  a.warps = P * D / 8 / (32 * kKvPieces);
+  if (a.warps < 1) a.warps = 1;
+  const int units = 8 / a.warps;
+  const dim3 grid(static_cast<unsigned>((batch->N + a.rows - 1) / a.rows),
+                  static_cast<unsigned>((2 * cache->kv_heads + units - 1) / units), 1);
   void* args[] = {&a};
-  cudaError_t e = launch_dependent3(fn, grid, T, 0, static_cast<cudaStream_t>(stream), args);
+  cudaError_t e = launch_dependent3(D == 64 ? reinterpret_cast<const void*>(&kv_append_kernel<64>)
+                                            : reinterpret_cast<const void*>(&kv_append_kernel<128>),
+                                    grid, kKvAppendThreads, 0, static_cast<cudaStream_t>(stream), args);
   if (e != cudaSuccess) return cuda_fail(e, "kv_append_kernel launch");
   return ok();
 }
@@ -261,9 +263,14 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache, const respin_kv_b
   a.v = static_cast<__nv_bfloat16*>(v_out);
   a.ldk = ld_k;
   a.ldv = ld_v;
-  const void* fn = cache->head_dim == 64 ? reinterpret_cast<const void*>(&kv_read_kernel<64>)
-                                         : reinterpret_cast<const void*>(&kv_read_kernel<128>);
-  const dim3 grid(static_cast<unsigned>((batch->N + kKvReadRows - 1) / kKvReadRows), 2, 1);
+  // 32 rows a block share the lookups; 8 where that leaves SMs without a block
+  const bool few = batch->N < 32 * 148;
+  const void* fn = cache->head_dim == 64 ? (few ? reinterpret_cast<const void*>(&kv_read_kernel<64, 8>)
+                                                : reinterpret_cast<const void*>(&kv_read_kernel<64, 32>))
+                                         : (few ? reinterpret_cast<const void*>(&kv_read_kernel<128, 8>)
+                                                : reinterpret_cast<const void*>(&kv_read_kernel<128, 32>));
+  const int R = few ? 8 : 32;
+  const dim3 grid(static_cast<unsigned>((batch->N + R - 1) / R), 2, 1);
   void* args[] = {&a};
   cudaError_t e = launch_dependent3(fn, grid, kKvReadThreads, 0, static_cast<cudaStream_t>(stream), args);
   if (e != cudaSuccess) return cuda_fail(e, "kv_read_kernel launch");
@@ -379,7 +386,7 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   const int joins = (few.blocks > 0 ? few.blocks - 1 : 0) + (many.blocks > 0 ? many.blocks - 1 : 0);
   if (joins > 0) {
     void* args[] = {&a, &few, &many};
-    const int y = many.blocks > 0 ? 8 : few.rows * D / 4 / 128;
+    const int y = many.blocks > 0 ? 32 : few.rows * D / 4 / 32;
     e = launch_dependent3(D == 64 ? reinterpret_cast<const void*>(&kv_combine_kernel<64>)
                                   : reinterpret_cast<const void*>(&kv_combine_kernel<128>),
                           dim3(static_cast<unsigned>(joins), static_cast<unsigned>(y), 1), 128, 0, s, args);

@@ -43,7 +43,7 @@
 namespace respin {
 
 constexpr int kKvTile = 64;          // tokens of a tile
-constexpr int kKvStages = 4;
+constexpr int kKvStages = 3;         // three blocks fit an SM (66 KB each at D = 128)
 constexpr int kKvWarps = 4;          // consumer warps, 16 tokens each
 constexpr int kKvThreads = (kKvWarps + 1) * 32;
 constexpr int kKvMaxBlocks = 592;    // 4 per SM
@@ -648,24 +648,51 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const KvAttnArgs a, con
   const long long slot = static_cast<long long>(RB) * (D + 2);
   const float* first = j.part + (2LL * (c - 1) + (f0 == u0 ? 0 : 1)) * slot;
   const float* rest = j.part + 2LL * c * slot;
-  for (int at = blockIdx.y * 128 + threadIdx.x; at < RB * (D / 4); at += gridDim.y * 128) {
+  // Few pieces: a thread for each (row, 4 dims). Many (a long context over many blocks): a warp takes 32
+  // of those and every fourth piece, and the four warps' sums meet in shared memory.
+  __shared__ float join[4][32][6];
+  const bool wide = pieces > 4;
+  const int lanes = wide ? 32 : 128, warp = threadIdx.x >> 5;
+  const int i0p = wide ? warp : 0, di = wide ? 4 : 1;
+  for (int base = blockIdx.y * lanes; base < RB * (D / 4); base += gridDim.y * lanes) {
+    const int at = base + (wide ? threadIdx.x & 31 : threadIdx.x);
     const int row = at % RB, d0 = at / RB * 4;
-    if (row >= rows) continue;
+    const bool live = at < RB * (D / 4) && row < rows;
     float M = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-      const float* p = i == 0 ? first : rest + 2LL * (i - 1) * slot;
-      const float2 ml = reinterpret_cast<const float2*>(p + RB * D)[row];
-      const float4 x = reinterpret_cast<const float4*>(p)[at];
-      const float Mn = fmaxf(M, ml.x);
-      const float f = M == -INFINITY ? 0.0f : ex2(M - Mn), g = ml.x == -INFINITY ? 0.0f : ex2(ml.x - Mn);
+    auto add = [&](float m2, float l2, const float4& x) {
+      const float Mn = fmaxf(M, m2);
+      const float f = M == -INFINITY ? 0.0f : ex2(M - Mn), g = m2 == -INFINITY ? 0.0f : ex2(m2 - Mn);
       M = Mn;
-      l = l * f + ml.y * g;
+      l = l * f + l2 * g;
       o[0] = o[0] * f + x.x * g;
       o[1] = o[1] * f + x.y * g;
       o[2] = o[2] * f + x.z * g;
       o[3] = o[3] * f + x.w * g;
+    };
+    if (live) {
+#pragma unroll 4
+      for (int i = i0p; i < pieces; i += di) {
+        const float* p = i == 0 ? first : rest + 2LL * (i - 1) * slot;
+        const float2 ml = reinterpret_cast<const float2*>(p + RB * D)[row];
+        add(ml.x, ml.y, reinterpret_cast<const float4*>(p)[at]);
+      }
     }
+    if (wide) {   // the same for the whole block
+      float* mine = join[warp][threadIdx.x & 31];
+      mine[0] = M;
+      mine[1] = l;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mine[2 + k] = o[k];
+      __syncthreads();
+      if (warp == 0)
+        for (int w = 1; w < 4; ++w) {
+          const float* p = join[w][threadIdx.x];
+          add(p[0], p[1], make_float4(p[2], p[3], p[4], p[5]));
+        }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
+    if (!live) continue;
     const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
     const int gr = pl.y + row;
     const long long tok = begin + gr / a.G;

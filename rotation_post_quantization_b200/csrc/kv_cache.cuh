@@ -86,7 +86,8 @@ __device__ __forceinline__ int kv_page(const KvView& c, int b, int t) {
   return -1;
 }
 
-constexpr int kKvScaleChunks = 8;   // 16-byte pieces of new values a thread holds
+constexpr int kKvPieces = 8;         // 16-byte pieces of new values a thread holds
+constexpr int kKvAppendThreads = 256;
 
 struct KvAppendArgs {
   KvView c;
@@ -94,6 +95,7 @@ struct KvAppendArgs {
   const __nv_bfloat16* v;
   long long ldk, ldv;   // elements between tokens
   int rows;             // rows of a block
+  int warps;            // of a unit (a head's K or V): P * D / 8 pieces at kKvPieces a lane, 1, 2, 4 or 8
 };
 
 // max |x| of eight bf16 values, finite ones only, as the bits of a bf16.
@@ -114,17 +116,24 @@ __device__ __forceinline__ uint32_t kv_code(float x, float inv) {
   return static_cast<uint32_t>(max(-127, min(127, q))) & 0xFFu;
 }
 
-// grid (row chunks, heads, K | V). The block's rows are cut at page
+// grid (row chunks, groups of units). The block's rows are cut at page
 // boundaries and sequence ends; it owns the pages whose first new token is
-// one of its rows. T threads hold a page's new values in registers
-// (P * D / 8 <= kKvScaleChunks * T), so the second look at them is free.
-template <int D, int T>
-__global__ void __launch_bounds__(T) kv_append_kernel(const KvAppendArgs a) {
+// one of its rows. Its eight warps are shared out over units (a head's keys or
+// values), so a page's place is looked up once for 8 / warps of them, and the
+// new values are on their way before the page's id and scale are asked for.
+// They stay in registers between the maximum and the codes. (A block for each
+// unit, everything in order: 122 us for 6906 tokens of 32 heads, 1.4 TB/s.)
+template <int D>
+__global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvAppendArgs a) {
   constexpr int L = D / 8;   // 16-byte pieces of a token
-  __shared__ uint32_t amax_warp[T / 32];
+  __shared__ uint32_t amax_warp[kKvAppendThreads / 32];
   const KvView& c = a.c;
-  const int tid = threadIdx.x, h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
+  const int warp = threadIdx.x / 32;
+  const int unit = blockIdx.y * (8 / a.warps) + warp / a.warps;   // head, K | V
+  const bool on = unit < 2 * c.H;
+  const int h = on ? unit >> 1 : 0;
+  const bool is_v = unit & 1;
+  const int T = a.warps * 32, tid = threadIdx.x % T;              // threads of the unit
   const __nv_bfloat16* src = (is_v ? a.v : a.k) + static_cast<long long>(h) * D;
   const long long ld = is_v ? a.ldv : a.ldk;
   int8_t* const codes0 = is_v ? c.v : c.k;
@@ -155,33 +164,35 @@ __global__ void __launch_bounds__(T) kv_append_kernel(const KvAppendArgs a) {
       r += n;
       continue;
     }
+    const int pieces = on ? n * L : 0;
+    uint4 buf[kKvPieces];
+#pragma unroll
+    for (int i = 0; i < kKvPieces; ++i) {
+      const int p = tid + i * T;
+      buf[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p < pieces) buf[i] = reinterpret_cast<const uint4*>(src + (r + p / L) * ld)[p % L];
+    }
     const int page = kv_page(c, b, pos);
-    if (page >= 0) {
-      int8_t* codes = codes0 + (static_cast<long long>(page) * c.H + h) * c.P * D;
-      float* scale = scales0 + static_cast<long long>(page) * c.H + h;
-      const float s_old = slot > 0 ? *scale : 0.0f;
-      const int pieces = n * L;
-      uint4 buf[kKvScaleChunks];
-      uint32_t m = 0;
+    const long long ph = static_cast<long long>(page < 0 ? 0 : page) * c.H + h;
+    int8_t* codes = codes0 + ph * c.P * D;
+    float* scale = scales0 + ph;
+    const float s_old = slot > 0 && page >= 0 ? *scale : 0.0f;
+    uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < kKvScaleChunks; ++i) {
-        const int p = tid + i * T;
-        buf[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (p < pieces) buf[i] = reinterpret_cast<const uint4*>(src + (r + p / L) * ld)[p % L];
-      }
-#pragma unroll
-      for (int i = 0; i < kKvScaleChunks; ++i) m = max(m, bf16x8_finite_amax(buf[i]));
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      if ((tid & 31) == 0) amax_warp[tid / 32] = m;
+    for (int i = 0; i < kKvPieces; ++i) m = max(m, bf16x8_finite_amax(buf[i]));
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (a.warps > 1) {
+      if ((threadIdx.x & 31) == 0) amax_warp[warp] = m;
       __syncthreads();
-#pragma unroll
-      for (int w = 0; w < T / 32; ++w) m = max(m, amax_warp[w]);
+      for (int w = 0; w < a.warps; ++w) m = max(m, amax_warp[warp / a.warps * a.warps + w]);
+    }
+    if (on && page >= 0) {
       float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
       if (s < 1.17549435e-38f) s = 0.0f;
       const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
       const float ratio = s > 0.0f ? __fdiv_rn(s_old, s) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < kKvScaleChunks; ++i) {
+      for (int i = 0; i < kKvPieces; ++i) {
         const int p = tid + i * T;
         if (p < pieces) {
           float x[8];
@@ -195,18 +206,22 @@ __global__ void __launch_bounds__(T) kv_append_kernel(const KvAppendArgs a) {
         }
       }
       if (slot > 0 && ratio != 1.0f) {   // the page's earlier tokens take the larger scale
-        for (int p = tid; p < slot * (D / 4); p += T) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(codes) + p;
-          const uint32_t w = *at;
-          uint32_t o = 0;
+        for (int p = tid; p < slot * (D / 16); p += T) {
+          uint4* at = reinterpret_cast<uint4*>(codes) + p;
+          const uint4 w = *at;
+          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+          uint32_t o[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o |= kv_code(static_cast<float>(static_cast<int8_t>(w >> (8 * j))), ratio) << (8 * j);
-          *at = o;
+          for (int j = 0; j < 16; ++j)
+            o[j / 4] |= kv_code(static_cast<float>(static_cast<int8_t>(in[j / 4] >> (8 * (j % 4)))), ratio) << (8 * (j % 4));
+          *at = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      __syncthreads();   // every thread has read the old scale and the maxima
-      if (tid == 0) *scale = s;
+    }
+    if (a.warps > 1) __syncthreads(); else __syncwarp();   // the unit has read its old scale and the maxima
+    if (on && page >= 0 && tid == 0) {
+      float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
+      *scale = s < 1.17549435e-38f ? 0.0f : s;
     }
     r += n;
   }
@@ -219,38 +234,38 @@ struct KvReadArgs {
   long long ldk, ldv;
 };
 
-constexpr int kKvReadRows = 16;
 constexpr int kKvReadThreads = 128;
 
-// grid (chunks of 16 rows, K | V). The rows' pages are found first; then the
-// block walks heads, rows and 16-byte pieces of codes: neighbouring rows of a
-// page are neighbours in memory, so a head's 16 rows are one run of codes.
-template <int D>
+// grid (chunks of R rows, K | V). One search finds the first row's sequence;
+// each row's lane walks on from there and looks its page up, so the rows'
+// lookups run side by side. Then the block walks heads, rows and 16-byte
+// pieces of codes: neighbouring rows of a page are neighbours in memory, so a
+// head's rows are one run of codes.
+template <int D, int R>
 __global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArgs a) {
   constexpr int L = D / 16;   // 16-byte pieces of a token's codes
-  __shared__ int page_of[kKvReadRows], slot_of[kKvReadRows];
+  __shared__ int page_of[R], slot_of[R];
   const KvView& c = a.c;
-  const int tid = threadIdx.x, warp = tid / 32;
+  const int tid = threadIdx.x;
   const bool is_v = blockIdx.y != 0;
   const int8_t* const codes = is_v ? c.v : c.k;
   const float* const scales = is_v ? c.v_scale : c.k_scale;
   __nv_bfloat16* const out = is_v ? a.v : a.k;
   const long long ld = is_v ? a.ldv : a.ldk;
-  const int r0 = blockIdx.x * kKvReadRows;
+  const int r0 = blockIdx.x * R;
 
   grid_dep_wait();
   grid_dep_launch();
-  int begin = 0, end = 0, len = 0, b = 0;
-  constexpr int kPerWarp = kKvReadRows / (kKvReadThreads / 32);
-  for (int i = 0; i < kPerWarp; ++i) {
-    const int r = r0 + warp * kPerWarp + i;
+  if (tid < 32) {
+    int b = kv_find(c, r0);
+    const int r = r0 + tid;
     int page = -1, slot = 0;
-    if (r < c.N) {
-      if (r < begin || r >= end) {
-        b = kv_find(c, r);
-        if (b >= c.B || !kv_rows(c, b, begin, end, len)) begin = end = 0;
-      }
-      if (r >= begin && r < end) {
+    if (tid < R && r < c.N) {
+      if (c.cu == nullptr) b = r / c.per;
+      else
+        while (b < c.B && c.cu[b + 1] <= r) ++b;
+      int begin, end, len;
+      if (b < c.B && kv_rows(c, b, begin, end, len) && r >= begin && r < end) {
         const int pos = len - (end - r);
         if (pos >= 0) {
           page = kv_page(c, b, pos);
@@ -260,16 +275,16 @@ __global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArg
         }
       }
     }
-    if ((tid & 31) == 0) {
-      page_of[warp * kPerWarp + i] = page;
-      slot_of[warp * kPerWarp + i] = slot;
+    if (tid < R) {
+      page_of[tid] = page;
+      slot_of[tid] = slot;
     }
   }
   __syncthreads();
-  const int total = c.H * kKvReadRows * L;
+  const int total = c.H * R * L;
 #pragma unroll 4
   for (int p = tid; p < total; p += kKvReadThreads) {
-    const int piece = p % L, row = (p / L) % kKvReadRows, h = p / (L * kKvReadRows);
+    const int piece = p % L, row = (p / L) % R, h = p / (L * R);
     const int page = page_of[row];
     if (page < 0) continue;
     const long long ph = static_cast<long long>(page) * c.H + h;

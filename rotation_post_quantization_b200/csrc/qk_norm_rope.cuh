@@ -25,7 +25,7 @@
 namespace respin {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;
+constexpr int kRopeUnroll = 2;
 
 struct RopeArgs {
   const __nv_bfloat16* q;
@@ -55,7 +55,7 @@ __device__ __forceinline__ float2 rope_cos_sin(int position, float freq) {
 }
 
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int L = D / 8;                         // lanes of one vector
   constexpr int V = kRopeThreads / L;              // vectors of one pass of the block
   extern __shared__ float2 rope_cs[];              // [tokens][rot / 2]
