@@ -151,7 +151,7 @@ KvLayout kv_layout(int D, long long rows) {
   const int v0 = D == 64 ? 0 : 3;
   l.few = rows <= 8 ? v0 : v0 + 1;
   l.many = rows > kKvFewRows ? v0 + 2 : -1;
-  l.part_few = 32LL * (kKvMaxBlocks + kTcaMaxBlocks);
+  l.part_few = 16LL * kKvPlan * (kKvMaxBlocks + kTcaMaxBlocks);
   l.part_many = l.part_few + 2LL * kKvMaxBlocks * kv_variant(l.few).slot * 4;
   l.bytes = l.part_many + (l.many < 0 ? 0 : 2LL * kTcaMaxBlocks * kv_variant(l.many).slot * 4);
   return l;
@@ -193,10 +193,9 @@ respin_status_t respin_qk_norm_rope(const void* q, const void* k, int N, int q_h
   RopeArgs a{static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<bf16*>(q_out), static_cast<bf16*>(k_out),
              static_cast<const bf16*>(q_weight), static_cast<const bf16*>(k_weight), positions, inv_freq,
              ld_q, ld_k, ld_qo, ld_ko, N, q_heads, kv_heads, rot_dim, 1, eps};
-  // Many tokens: four of them a block, so the 256 threads form a sine and
-  // cosine each for a full 128-wide rotation. Few: one, and its vectors go to
-  // several blocks.
-  a.tokens = N >= 592 ? 4 : 1;
+  // Many tokens: as many a block as make one wave of six blocks on each of 148 SMs, at most 8 (their
+  // sines and cosines are formed once for all heads). Few: one, and its vectors go to several blocks.
+  a.tokens = N < 592 ? 1 : N >= 8 * 888 ? 8 : (N + 887) / 888;
   const int V = kRopeThreads / (head_dim / 8);
   const int passes = (a.tokens * (q_heads + kv_heads) + V - 1) / V;
   const int y = N >= 592 ? 1 : passes;
@@ -235,9 +234,12 @@ respin_status_t respin_kv_append(const respin_kv_cache_t* cache, const respin_kv
   a.rows = per < 1 ? 1 : per > P ? P : per;
   a.warps = P * D / 8 / (32 * kKvPieces);
   if (a.warps < 1) a.warps = 1;
-  const int units = 8 / a.warps;
-  const dim3 grid(static_cast<unsigned>((batch->N + a.rows - 1) / a.rows),
-                  static_cast<unsigned>((2 * cache->kv_heads + units - 1) / units), 1);
+  // Groups of units side by side until there are three blocks for each of 148 SMs; the rest in turn.
+  const int units = 8 / a.warps, groups = (2 * cache->kv_heads + units - 1) / units;
+  const int chunks = (batch->N + a.rows - 1) / a.rows;
+  int y = (3 * 148 + chunks - 1) / chunks;
+  if (y > groups) y = groups;
+  const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>(y), 1);
   void* args[] = {&a};
   cudaError_t e = launch_dependent3(D == 64 ? reinterpret_cast<const void*>(&kv_append_kernel<64>)
                                             : reinterpret_cast<const void*>(&kv_append_kernel<128>),
@@ -263,14 +265,17 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache, const respin_kv_b
   a.v = static_cast<__nv_bfloat16*>(v_out);
   a.ldk = ld_k;
   a.ldv = ld_v;
-  // 32 rows a block share the lookups; 8 where that leaves SMs without a block
+  // 32 rows a block share the lookups; 8 where that leaves SMs without a block. A block takes as many
+  // heads as make 1024 pieces of 16 bytes (8 a thread): more of them hide one another's lookups.
   const bool few = batch->N < 32 * 148;
   const void* fn = cache->head_dim == 64 ? (few ? reinterpret_cast<const void*>(&kv_read_kernel<64, 8>)
                                                 : reinterpret_cast<const void*>(&kv_read_kernel<64, 32>))
                                          : (few ? reinterpret_cast<const void*>(&kv_read_kernel<128, 8>)
                                                 : reinterpret_cast<const void*>(&kv_read_kernel<128, 32>));
   const int R = few ? 8 : 32;
-  const dim3 grid(static_cast<unsigned>((batch->N + R - 1) / R), 2, 1);
+  a.heads = 1024 / (R * cache->head_dim / 16);
+  const dim3 grid(static_cast<unsigned>((batch->N + R - 1) / R), 2,
+                  static_cast<unsigned>((cache->kv_heads + a.heads - 1) / a.heads));
   void* args[] = {&a};
   cudaError_t e = launch_dependent3(fn, grid, kKvReadThreads, 0, static_cast<cudaStream_t>(stream), args);
   if (e != cudaSuccess) return cuda_fail(e, "kv_read_kernel launch");
@@ -351,8 +356,8 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   cudaStream_t s = static_cast<cudaStream_t>(stream);
 
   // Sequences of many rows, then those of few; a uniform batch has one kind.
-  KvJoin few{reinterpret_cast<int4*>(ws), reinterpret_cast<float*>(ws + lay.part_few), 0, kv_variant(lay.few).rows};
-  KvJoin many{reinterpret_cast<int4*>(ws + 32 * kKvMaxBlocks), reinterpret_cast<float*>(ws + lay.part_many), 0, kTcaGroup};
+  KvJoin few{reinterpret_cast<int4*>(ws), reinterpret_cast<float*>(ws + lay.part_few), 0, kv_variant(lay.few).rows, 0};
+  KvJoin many{reinterpret_cast<int4*>(ws + 16 * kKvPlan * kKvMaxBlocks), reinterpret_cast<float*>(ws + lay.part_many), 0, kTcaGroup, 0};
   const uint64_t rows = static_cast<uint64_t>(cache->num_pages) * H * cache->page_size;
   const uint32_t box = cache->page_size < kKvTile ? cache->page_size : kKvTile;   // both kernels' 64-token tiles
   CUtensorMap tmK, tmV;
@@ -383,13 +388,14 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
     e = launch_dependent3(v.fn, dim3(static_cast<unsigned>(few.blocks), 1, 1), v.threads, v.smem, s, args);
     if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
   }
-  const int joins = (few.blocks > 0 ? few.blocks - 1 : 0) + (many.blocks > 0 ? many.blocks - 1 : 0);
+  few.parts = few.rows * D / 4 / 64;   // 2 or 4 at head_dim 128
+  many.parts = D / 8;
+  const int joins = (few.blocks > 0 ? (few.blocks - 1) * few.parts : 0) + (many.blocks > 0 ? (many.blocks - 1) * many.parts : 0);
   if (joins > 0) {
     void* args[] = {&a, &few, &many};
-    const int y = many.blocks > 0 ? 32 : few.rows * D / 4 / 32;
     e = launch_dependent3(D == 64 ? reinterpret_cast<const void*>(&kv_combine_kernel<64>)
                                   : reinterpret_cast<const void*>(&kv_combine_kernel<128>),
-                          dim3(static_cast<unsigned>(joins), static_cast<unsigned>(y), 1), 128, 0, s, args);
+                          dim3(static_cast<unsigned>(joins), 1, 1), kKvJoinThreads, 0, s, args);
     if (e != cudaSuccess) return cuda_fail(e, "kv_combine_kernel launch");
   }
   return ok();

@@ -49,6 +49,7 @@ constexpr int kKvThreads = (kKvWarps + 1) * 32;
 constexpr int kKvMaxBlocks = 592;    // 4 per SM
 constexpr int kKvMinTiles = 4;       // least piece of a block
 constexpr int kKvFewRows = 16;       // rows a key head up to which a sequence is this kernel's
+constexpr int kKvPlan = 3;           // int4s a block leaves about its piece (KvJoin)
 constexpr float kKvBias = 6.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^14 in fp16
 constexpr float kKvLazy = 8.0f;      // the running maximum may lag by 2^8
 
@@ -64,7 +65,7 @@ struct KvAttnArgs {
   unsigned long long div_g;   // ceil(2^64 / G), 0 for G = 1
   int few_rows;          // sequences of more rows (tokens * G) are another kernel's
   int others;            // whether that kernel runs; else such a sequence is refused
-  int4* plan;            // workspace: [blocks][2] where a block's piece begins
+  int4* plan;            // workspace: [blocks][kKvPlan] where a block's piece begins
   float* part;           // workspace: [blocks][2] partial results
 };
 
@@ -273,9 +274,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         const int unit = static_cast<int>(off / s.tiles);
         pl = make_int4(b_at, unit / a.c.H * C::RB, unit % a.c.H, static_cast<int>(off % s.tiles));
         pm.x = s.tiles;
+        pm.w = 1 + static_cast<int>((s.tiles - pl.w + chunk - 1) / chunk);
+        a.plan[kKvPlan * blockIdx.x + 2] = make_int4(s.begin, s.rows, 0, 0);
       }
-      a.plan[2 * blockIdx.x] = pl;
-      a.plan[2 * blockIdx.x + 1] = pm;
+      a.plan[kKvPlan * blockIdx.x] = pl;
+      a.plan[kKvPlan * blockIdx.x + 1] = pm;
     }
   }
   __syncthreads();
@@ -607,54 +610,59 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 }
 
 // Joins the partial results of units that several blocks of a kernel share.
-// Block (i, y) of `blocks` pieces: the unit that piece i + 1 begins inside of,
-// if that is the second of the unit's pieces; every gridDim.y-th part of its
-// rows and dims.
+// Of `blocks` pieces: the unit that piece c begins inside of, if that is the
+// second of the unit's pieces; `parts` blocks share its rows and dims.
 struct KvJoin {
+  // [blocks]: (sequence or -1, first row, head, tiles of the unit before the piece); (the unit's tiles,
+  // the line's tiles before the piece in two halves, pieces from the unit's start on or 0: to be
+  // counted); (the sequence's first row of the batch, its rows)
   const int4* plan;
   const float* part;
   int blocks, rows;   // pieces; rows of a partial result
+  int parts;
 };
 
+constexpr int kKvJoinThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(128) kv_combine_kernel(const KvAttnArgs a, const KvJoin few, const KvJoin many) {
+__global__ void __launch_bounds__(kKvJoinThreads) kv_combine_kernel(const KvAttnArgs a, const KvJoin few, const KvJoin many) {
   grid_dep_wait();
   grid_dep_launch();
-  const int i0 = blockIdx.x;
-  const KvJoin j = i0 < few.blocks - 1 ? few : many;
-  const int c = (i0 < few.blocks - 1 ? i0 : i0 - max(0, few.blocks - 1)) + 1;
-  const int4 pl = j.plan[2 * c], pm = j.plan[2 * c + 1];
+  const int n_few = max(0, few.blocks - 1) * few.parts, i0 = blockIdx.x;
+  const KvJoin j = i0 < n_few ? few : many;
+  const int at0 = i0 < n_few ? i0 : i0 - n_few, part = at0 % j.parts, c = at0 / j.parts + 1;
+  // (asked for together; the last two are unused where the first says so)
+  const int4 pl = j.plan[kKvPlan * c], pm = j.plan[kKvPlan * c + 1], pr = j.plan[kKvPlan * c + 2],
+             pb = j.plan[kKvPlan * (c - 1) + 1];
   const int z = pl.w, tiles = pm.x;
   if (pl.x < 0 || z == 0) return;   // no piece, or one that begins with a unit
   // the unit's tiles [u0, u1) of the line; pieces c - 1, c, ... begin at from(c - 1), ...
-  auto from = [&](int i) {
-    const int4 m = j.plan[2 * i + 1];
-    return (static_cast<long long>(m.z) << 32) | static_cast<unsigned>(m.y);
-  };
-  const long long u0 = from(c) - z, u1 = u0 + tiles, f0 = from(c - 1);
+  auto from = [](const int4& m) { return (static_cast<long long>(m.z) << 32) | static_cast<unsigned>(m.y); };
+  const long long u0 = from(pm) - z, u1 = u0 + tiles, f0 = from(pb);
   if (f0 > u0) return;              // a later piece of the unit
-  int begin, end, len;
-  kv_rows(a.c, pl.x, begin, end, len);
-  const int rows = (end - begin) * a.G - pl.y;
-  const int RB = j.rows;
-  int pieces = 1;
-  for (int i = c; i < j.blocks; i += 32) {   // 32 pieces looked at in a step
-    const int l = i + static_cast<int>(threadIdx.x & 31);
-    const int n = __popc(__ballot_sync(0xFFFFFFFFu, l < j.blocks && from(l) < u1));
-    pieces += n;
-    if (n < 32) break;
+  const int begin = pr.x, rows = pr.y - pl.y, RB = j.rows;
+  int pieces = pm.w;
+  if (pieces == 0) {
+    pieces = 1;
+    for (int i = c; i < j.blocks; i += 32) {   // 32 looked at in a step
+      const int l = i + static_cast<int>(threadIdx.x & 31);
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, l < j.blocks && from(j.plan[kKvPlan * l + 1]) < u1));
+      pieces += n;
+      if (n < 32) break;
+    }
   }
   // their results: of piece c - 1 its last segment (the second slot unless it begins with the unit), of the others the first
   const long long slot = static_cast<long long>(RB) * (D + 2);
   const float* first = j.part + (2LL * (c - 1) + (f0 == u0 ? 0 : 1)) * slot;
   const float* rest = j.part + 2LL * c * slot;
   // Few pieces: a thread for each (row, 4 dims). Many (a long context over many blocks): a warp takes 32
-  // of those and every fourth piece, and the four warps' sums meet in shared memory.
-  __shared__ float join[4][32][6];
+  // of those and every eighth piece, and the warps' sums meet in shared memory.
+  constexpr int W = kKvJoinThreads / 32;
+  __shared__ float join[W][32][6];
   const bool wide = pieces > 4;
-  const int lanes = wide ? 32 : 128, warp = threadIdx.x >> 5;
-  const int i0p = wide ? warp : 0, di = wide ? 4 : 1;
-  for (int base = blockIdx.y * lanes; base < RB * (D / 4); base += gridDim.y * lanes) {
+  const int lanes = wide ? 32 : kKvJoinThreads, warp = threadIdx.x >> 5;
+  const int i0p = wide ? warp : 0, di = wide ? W : 1;
+  for (int base = part * lanes; base < RB * (D / 4); base += j.parts * lanes) {
     const int at = base + (wide ? threadIdx.x & 31 : threadIdx.x);
     const int row = at % RB, d0 = at / RB * 4;
     const bool live = at < RB * (D / 4) && row < rows;
@@ -685,7 +693,7 @@ __global__ void __launch_bounds__(128) kv_combine_kernel(const KvAttnArgs a, con
       for (int k = 0; k < 4; ++k) mine[2 + k] = o[k];
       __syncthreads();
       if (warp == 0)
-        for (int w = 1; w < 4; ++w) {
+        for (int w = 1; w < W; ++w) {
           const float* p = join[w][threadIdx.x];
           add(p[0], p[1], make_float4(p[2], p[3], p[4], p[5]));
         }

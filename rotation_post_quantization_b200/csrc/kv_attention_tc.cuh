@@ -313,8 +313,12 @@ __device__ __forceinline__ void tca_locate(const KvAttnArgs& a, volatile int* sh
     sh[2] = at[0].h;
     sh[3] = at[0].z;
     sh[4] = static_cast<int>(end - first);
-    a.plan[2 * blockIdx.x] = make_int4(at[0].b, at[0].g * kTcaGroup, at[0].h, at[0].z);
-    a.plan[2 * blockIdx.x + 1] = make_int4(at[0].tiles, static_cast<int>(first & 0xFFFFFFFF), static_cast<int>(first >> 32), 0);
+    a.plan[kKvPlan * blockIdx.x] = make_int4(at[0].b, at[0].g * kTcaGroup, at[0].h, at[0].z);
+    a.plan[kKvPlan * blockIdx.x + 1] = make_int4(at[0].tiles, static_cast<int>(first & 0xFFFFFFFF), static_cast<int>(first >> 32), 0);
+    if (at[0].b >= 0) {
+      const TcaSeq s = tca_seq(a, at[0].b);
+      a.plan[kKvPlan * blockIdx.x + 2] = make_int4(s.begin, s.rows, 0, 0);
+    }
   }
 }
 

@@ -119,25 +119,18 @@ __device__ __forceinline__ uint32_t kv_code(float x, float inv) {
 // grid (row chunks, groups of units). The block's rows are cut at page
 // boundaries and sequence ends; it owns the pages whose first new token is
 // one of its rows. Its eight warps are shared out over units (a head's keys or
-// values), so a page's place is looked up once for 8 / warps of them, and the
-// new values are on their way before the page's id and scale are asked for.
-// They stay in registers between the maximum and the codes. (A block for each
-// unit, everything in order: 122 us for 6906 tokens of 32 heads, 1.4 TB/s.)
+// values) and go from group to group of them, so a page's place is looked up
+// once for many. The new values stay in registers between the maximum and the
+// codes. (A block for each unit, with its own lookups: 122 us for 6906 tokens
+// of 32 heads, 1.4 TB/s.)
 template <int D>
-__global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvAppendArgs a) {
+__global__ void __launch_bounds__(kKvAppendThreads, 3) kv_append_kernel(const KvAppendArgs a) {
   constexpr int L = D / 8;   // 16-byte pieces of a token
   __shared__ uint32_t amax_warp[kKvAppendThreads / 32];
   const KvView& c = a.c;
   const int warp = threadIdx.x / 32;
-  const int unit = blockIdx.y * (8 / a.warps) + warp / a.warps;   // head, K | V
-  const bool on = unit < 2 * c.H;
-  const int h = on ? unit >> 1 : 0;
-  const bool is_v = unit & 1;
-  const int T = a.warps * 32, tid = threadIdx.x % T;              // threads of the unit
-  const __nv_bfloat16* src = (is_v ? a.v : a.k) + static_cast<long long>(h) * D;
-  const long long ld = is_v ? a.ldv : a.ldk;
-  int8_t* const codes0 = is_v ? c.v : c.k;
-  float* const scales0 = is_v ? c.v_scale : c.k_scale;
+  const int T = a.warps * 32, tid = threadIdx.x % T;   // threads of a unit
+  const int units = 8 / a.warps;                       // of the block at a time
 
   grid_dep_wait();
   grid_dep_launch();
@@ -164,64 +157,74 @@ __global__ void __launch_bounds__(kKvAppendThreads) kv_append_kernel(const KvApp
       r += n;
       continue;
     }
-    const int pieces = on ? n * L : 0;
-    uint4 buf[kKvPieces];
-#pragma unroll
-    for (int i = 0; i < kKvPieces; ++i) {
-      const int p = tid + i * T;
-      buf[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p < pieces) buf[i] = reinterpret_cast<const uint4*>(src + (r + p / L) * ld)[p % L];
-    }
     const int page = kv_page(c, b, pos);
-    const long long ph = static_cast<long long>(page < 0 ? 0 : page) * c.H + h;
-    int8_t* codes = codes0 + ph * c.P * D;
-    float* scale = scales0 + ph;
-    const float s_old = slot > 0 && page >= 0 ? *scale : 0.0f;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < kKvPieces; ++i) m = max(m, bf16x8_finite_amax(buf[i]));
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (a.warps > 1) {
-      if ((threadIdx.x & 31) == 0) amax_warp[warp] = m;
-      __syncthreads();
-      for (int w = 0; w < a.warps; ++w) m = max(m, amax_warp[warp / a.warps * a.warps + w]);
-    }
-    if (on && page >= 0) {
-      float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
-      if (s < 1.17549435e-38f) s = 0.0f;
-      const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-      const float ratio = s > 0.0f ? __fdiv_rn(s_old, s) : 0.0f;
+    for (int u0 = blockIdx.y * units; u0 < 2 * c.H; u0 += gridDim.y * units) {
+      const int unit = u0 + warp / a.warps;   // head, K | V
+      const bool on = unit < 2 * c.H;
+      const int h = on ? unit >> 1 : 0;
+      const bool is_v = unit & 1;
+      const __nv_bfloat16* src = (is_v ? a.v : a.k) + static_cast<long long>(h) * D;
+      const long long ld = is_v ? a.ldv : a.ldk;
+      int8_t* const codes0 = is_v ? c.v : c.k;
+      float* const scales0 = is_v ? c.v_scale : c.k_scale;
+      const int pieces = on ? n * L : 0;
+      uint4 buf[kKvPieces];
 #pragma unroll
       for (int i = 0; i < kKvPieces; ++i) {
         const int p = tid + i * T;
-        if (p < pieces) {
-          float x[8];
-          uint32_t q[8];
-          bf16x8_to_f32(buf[i], x);
+        buf[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p < pieces) buf[i] = reinterpret_cast<const uint4*>(src + (r + p / L) * ld)[p % L];
+      }
+      const long long ph = static_cast<long long>(page < 0 ? 0 : page) * c.H + h;
+      int8_t* codes = codes0 + ph * c.P * D;
+      float* scale = scales0 + ph;
+      const float s_old = slot > 0 && page >= 0 ? *scale : 0.0f;
+      uint32_t m = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q[j] = s > 0.0f ? kv_code(x[j], inv) : 0u;
-          const uint2 w = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                                     q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
-          reinterpret_cast<uint2*>(codes + (slot + p / L) * D)[p % L] = w;
+      for (int i = 0; i < kKvPieces; ++i) m = max(m, bf16x8_finite_amax(buf[i]));
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if (a.warps > 1) {
+        if ((threadIdx.x & 31) == 0) amax_warp[warp] = m;
+        __syncthreads();
+        for (int w = 0; w < a.warps; ++w) m = max(m, amax_warp[warp / a.warps * a.warps + w]);
+      }
+      if (on && page >= 0) {
+        float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
+        if (s < 1.17549435e-38f) s = 0.0f;
+        const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        const float ratio = s > 0.0f ? __fdiv_rn(s_old, s) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < kKvPieces; ++i) {
+          const int p = tid + i * T;
+          if (p < pieces) {
+            float x[8];
+            uint32_t q[8];
+            bf16x8_to_f32(buf[i], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) q[j] = s > 0.0f ? kv_code(x[j], inv) : 0u;
+            const uint2 w = make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
+                                       q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+            reinterpret_cast<uint2*>(codes + (slot + p / L) * D)[p % L] = w;
+          }
+        }
+        if (slot > 0 && ratio != 1.0f) {   // the page's earlier tokens take the larger scale
+          for (int p = tid; p < slot * (D / 16); p += T) {
+            uint4* at = reinterpret_cast<uint4*>(codes) + p;
+            const uint4 w = *at;
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t o[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              o[j / 4] |= kv_code(static_cast<float>(static_cast<int8_t>(in[j / 4] >> (8 * (j % 4)))), ratio) << (8 * (j % 4));
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
       }
-      if (slot > 0 && ratio != 1.0f) {   // the page's earlier tokens take the larger scale
-        for (int p = tid; p < slot * (D / 16); p += T) {
-          uint4* at = reinterpret_cast<uint4*>(codes) + p;
-          const uint4 w = *at;
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          uint32_t o[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            o[j / 4] |= kv_code(static_cast<float>(static_cast<int8_t>(in[j / 4] >> (8 * (j % 4)))), ratio) << (8 * (j % 4));
-          *at = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+      if (a.warps > 1) __syncthreads(); else __syncwarp();   // the unit has read its old scale and the maxima
+      if (on && page >= 0 && tid == 0) {
+        float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
+        *scale = s < 1.17549435e-38f ? 0.0f : s;
       }
-    }
-    if (a.warps > 1) __syncthreads(); else __syncwarp();   // the unit has read its old scale and the maxima
-    if (on && page >= 0 && tid == 0) {
-      float s = fmaxf(s_old, __fdiv_rn(__uint_as_float(m << 16), 127.0f));
-      *scale = s < 1.17549435e-38f ? 0.0f : s;
     }
     r += n;
   }
@@ -232,11 +235,12 @@ struct KvReadArgs {
   __nv_bfloat16* k;
   __nv_bfloat16* v;
   long long ldk, ldv;
+  int heads;   // of a block
 };
 
 constexpr int kKvReadThreads = 128;
 
-// grid (chunks of R rows, K | V). One search finds the first row's sequence;
+// grid (chunks of R rows, K | V, groups of heads). One search finds the first row's sequence;
 // each row's lane walks on from there and looks its page up, so the rows'
 // lookups run side by side. Then the block walks heads, rows and 16-byte
 // pieces of codes: neighbouring rows of a page are neighbours in memory, so a
@@ -281,28 +285,44 @@ __global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArg
     }
   }
   __syncthreads();
-  const int total = c.H * R * L;
-#pragma unroll 4
-  for (int p = tid; p < total; p += kKvReadThreads) {
-    const int piece = p % L, row = (p / L) % R, h = p / (L * R);
-    const int page = page_of[row];
-    if (page < 0) continue;
-    const long long ph = static_cast<long long>(page) * c.H + h;
-    const uint4 w = reinterpret_cast<const uint4*>(codes + (ph * c.P + slot_of[row]) * D)[piece];
-    const float s = scales[ph];
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
+  // this block's heads
+  const int h0 = blockIdx.z * a.heads, nh = min(a.heads, c.H - h0);
+  const int total = nh * R * L;
+  constexpr int U = 4;   // pieces of a thread in flight
+  for (int p0 = tid; p0 < total; p0 += U * kKvReadThreads) {
+    uint4 w[U];
+    float s[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(in[i] >> (8 * j))), s);
-      o[2 * i] = pack_bf16x2(x[0], x[1]);
-      o[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + u * kKvReadThreads;
+      const int row = (p / L) % R, h = h0 + p / (L * R);
+      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      s[u] = 0.0f;
+      if (p < total && page_of[row] >= 0) {
+        const long long ph = static_cast<long long>(page_of[row]) * c.H + h;
+        w[u] = reinterpret_cast<const uint4*>(codes + (ph * c.P + slot_of[row]) * D)[p % L];
+        s[u] = scales[ph];
+      }
     }
-    uint4* to = reinterpret_cast<uint4*>(out + (r0 + row) * ld + static_cast<long long>(h) * D) + 2 * piece;
-    to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = p0 + u * kKvReadThreads;
+      const int row = (p / L) % R, h = h0 + p / (L * R);
+      if (p >= total || page_of[row] < 0) continue;
+      const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(in[i] >> (8 * j))), s[u]);
+        o[2 * i] = pack_bf16x2(x[0], x[1]);
+        o[2 * i + 1] = pack_bf16x2(x[2], x[3]);
+      }
+      uint4* to = reinterpret_cast<uint4*>(out + (r0 + row) * ld + static_cast<long long>(h) * D) + 2 * (p % L);
+      to[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
   }
 }
 

@@ -68,9 +68,12 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const Rop
 
   grid_dep_wait();
   grid_dep_launch();
+  // A lane reads the angles of its 8 values (4 pairs interleaved): angle E l + i lies at i * (half / E) + l,
+  // so that neighbouring lanes read neighbouring ones.
+  constexpr int E = INTERLEAVED ? 4 : 8;
   for (int i = tid; i < nt * half; i += kRopeThreads) {
-    const int t = i / half;
-    rope_cs[i] = rope_cos_sin(a.positions[t0 + t], a.inv_freq[i - t * half]);
+    const int t = i / half, f = i - t * half;
+    rope_cs[t * half + (f % E) * (half / E) + f / E] = rope_cos_sin(a.positions[t0 + t], a.inv_freq[f]);
   }
   uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
   if (a.q_weight != nullptr) wq = reinterpret_cast<const uint4*>(a.q_weight)[li];
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const Rop
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float2 r = make_float2(1.0f, 0.0f);
-          if (8 * li + 2 * i < a.rot) r = cs[4 * li + i];
+          if (8 * li + 2 * i < a.rot) r = cs[i * (half / 4) + li];
           y[2 * i] = x[2 * i] * r.x - x[2 * i + 1] * r.y;
           y[2 * i + 1] = x[2 * i + 1] * r.x + x[2 * i] * r.y;
         }
@@ -153,10 +156,10 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const Rop
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xFFFFFFFFu, x[i], src);
         if (in) {
-          const float2* c = cs + (first ? 8 * li : 8 * (li - hl));
+          const float2* c = cs + (first ? li : li - hl);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float2 r = c[i];
+            const float2 r = c[i * hl];
             y[i] = first ? x[i] * r.x - y[i] * r.y : x[i] * r.x + y[i] * r.y;
           }
         } else {
