@@ -231,8 +231,14 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
   // ---- this block's piece of the line
   if (warp == 0) {
-    long long total = 0;
-    for (int b = lane; b < a.c.B; b += 32) total += kv_weight<C::RB>(a, b);
+    constexpr int kKept = 4;   // weights of the first 128 sequences stay in registers for the second look
+    long long total = 0, kept[kKept];
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+      kept[i] = 32 * i + lane < a.c.B ? kv_weight<C::RB>(a, 32 * i + lane) : 0;
+      total += kept[i];
+    }
+    for (int b = 32 * kKept + lane; b < a.c.B; b += 32) total += kv_weight<C::RB>(a, b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     const long long g = gridDim.x;
@@ -244,7 +250,11 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     if (left > 0) {
       long long before = 0;
       for (int b0 = 0; b0 < a.c.B; b0 += 32) {
-        const long long w = b0 + lane < a.c.B ? kv_weight<C::RB>(a, b0 + lane) : 0;
+        long long w = 0;
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+          if (b0 == 32 * i) w = kept[i];
+        if (b0 >= 32 * kKept && b0 + lane < a.c.B) w = kv_weight<C::RB>(a, b0 + lane);
         long long incl = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

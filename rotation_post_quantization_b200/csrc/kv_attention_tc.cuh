@@ -632,18 +632,16 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       constexpr int Per = kTcaTile * Pieces / 128;   // pieces of a thread
       constexpr int Step = 128 / Pieces;             // tokens between them
       const int c = pt % Pieces, tk = pt / Pieces;
-      // the two blocks of a row lie on the same banks: their lanes store the other half first
-      const bool flip = c >= 4;
       uint8_t* p = to + (c >> 2) * Block + (tk >> 3) * 1024 + (tk & 7) * 128;   // t & 7 = tk & 7
-      const int a0 = (((2 * (c & 3)) + (flip ? 1 : 0)) ^ (tk & 7)) << 4, a1 = a0 ^ 16;
+      const int a0 = ((2 * (c & 3)) ^ (tk & 7)) << 4;
 #pragma unroll
       for (int i = 0; i < Per; ++i) {
         const uint4 w = reinterpret_cast<const uint4*>(from)[pt + 128 * i];
         const uint32_t x[4] = {w.x ^ 0x80808080u, w.y ^ 0x80808080u, w.z ^ 0x80808080u, w.w ^ 0x80808080u};
         const uint4 lo = make_uint4(codes_f16x2<0>(x[0]), codes_f16x2<1>(x[0]), codes_f16x2<0>(x[1]), codes_f16x2<1>(x[1]));
         const uint4 hi = make_uint4(codes_f16x2<0>(x[2]), codes_f16x2<1>(x[2]), codes_f16x2<0>(x[3]), codes_f16x2<1>(x[3]));
-        *reinterpret_cast<uint4*>(p + i * Step * 128 + a0) = flip ? hi : lo;
-        *reinterpret_cast<uint4*>(p + i * Step * 128 + a1) = flip ? lo : hi;
+        *reinterpret_cast<uint4*>(p + i * Step * 128 + a0) = lo;
+        *reinterpret_cast<uint4*>(p + i * Step * 128 + (a0 ^ 16)) = hi;
       }
     };
     while (cur.left > 0 && ok) {
