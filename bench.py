@@ -75,7 +75,7 @@ def parse_args():
                         "with --workload llama2_70b the factor plan of that rank)")
     p.add_argument("--workload", default="llama2_7b",
                    choices=["llama2_7b", "llama2_7b_w3a3", "tiny", "decode", "llama2_70b",
-                            "llama3_8b_stack"],
+                            "llama3_8b_stack", "llama3_8b_attention"],
                    help="llama2_7b (default): the headline step; llama2_7b_w3a3: the "
                         "same step with 3-bit activation and weight codes. The others "
                         "print one JSON line each for the remaining workload "
@@ -1098,6 +1098,59 @@ def wl_stack(args, env, form: str, cpu: bool) -> dict:
     return out
 
 
+def wl_attention(args, env) -> dict:
+    """The attention half of a Llama-3-8B-shaped layer on its quantized path:
+    q/k/v projection (W4A4), position rotation, 8-bit cache append, attention,
+    per-token INT4 codes, output projection (W4A4). A decode step of 64
+    sequences behind 4096 tokens, and a prompt of 4096 tokens."""
+    import rotation_post_quantization_b200 as rq
+    torch, dev = env.torch, env.dev
+    D, H, Hk, d, P = 4096, 32, 8, 128, 64
+    quant = rq.Plan(D, 0)
+    freq = (500000.0 ** (-torch.arange(0, d, 2, device=dev, dtype=torch.float64) / d)).float()
+    wqkv, sqkv = env.codes((H + 2 * Hk) * d, D), env.wscales((H + 2 * Hk) * d)
+    wo, so = env.codes(D, D), env.wscales(D)
+    out = {"config": {"D": D, "q_heads": H, "kv_heads": Hk, "head_dim": d, "page_size": P,
+                      "cache": "int8, one scale a page and head"}}
+    for name, B, q, kv in (("decode_64x4096", 64, 1, 4096), ("prompt_4096", 1, 4096, 4096)):
+        N, pages = B * q, -(-kv // P)
+        cache = rq.KvCache.empty(B * pages, P, Hk, d, device=dev)
+        for t in (cache.k, cache.v):
+            t.random_(-127, 128, generator=env.g)
+        for t in (cache.k_scale, cache.v_scale):
+            t.fill_(0.02)
+        table = torch.randperm(B * pages, generator=env.g, device=dev).to(torch.int32).view(B, pages)
+        kv_len = torch.full((B,), kv, dtype=torch.int32, device=dev)
+        pos = (kv - q + torch.arange(q, device=dev, dtype=torch.int32)).repeat(B)
+        qa, sa = env.codes(N, D), torch.rand(N, generator=env.g, device=dev) + 0.5
+        qkv = torch.empty(N, (H + 2 * Hk) * d, dtype=torch.bfloat16, device=dev)
+        qh, kh, vh = (qkv[:, a * d:b * d].view(N, b - a, d) for a, b in ((0, H), (H, H + Hk), (H + Hk, H + 2 * Hk)))
+        at = torch.empty(N, H, d, dtype=torch.bfloat16, device=dev)
+        ws = torch.empty(rq.respin_kv_attention_workspace(cache, H, N, q), dtype=torch.uint8, device=dev)
+        _, qo, sc, y = env.outs(N, D, D)
+        stages = {
+            "qkv_gemm": lambda: rq.w4a4_gemm(qa, sa, wqkv, sqkv, qkv),
+            "rotation": lambda: rq.respin_qk_norm_rope(qh, kh, pos, freq, qh, kh),
+            "append": lambda: rq.respin_kv_append(cache, kh, vh, kv_len, table),
+            "attention": lambda: rq.respin_kv_attention(cache, qh, kv_len, table, at, ws),
+            "codes": lambda: rq.respin_boundary_forward(quant, at.view(N, D), None, None, qo, sc),
+            "out_gemm": lambda: rq.w4a4_gemm(qo, sc, wo, so, y)}
+
+        def layer(i):
+            for f in stages.values():
+                f()
+
+        for i in range(env.warmup):
+            layer(i)
+        us = {k: _graph_ms(torch, lambda i, f=f: f(), env.iters) * 1e3 for k, f in stages.items()}
+        out[name] = {"tokens": N, "layer_us": _graph_ms(torch, layer, env.iters) * 1e3, "stage_us": us,
+                     "cache_bytes_per_s": 2.0 * B * kv * Hk * d / us["attention"] * 1e6}
+    quant.destroy()
+    out["note"] = ("CUDA-graph replay, device time per call; the 64-sequence cache is 4x L2, the prompt's is "
+                   "L2-resident")
+    return out
+
+
 def all_workloads(args, form: str, cpu: bool) -> dict:
     """Configurations 1, 3, 4, 5 (compact), appended to the headline line."""
     env = _Env(args)
@@ -1122,7 +1175,8 @@ def run_workload(args):
     cpu = not args.no_cpu_baseline
     fn = {"tiny": lambda: wl_tiny(args, env, cpu), "decode": lambda: wl_decode(args, env, form, cpu),
           "llama2_70b": lambda: wl_70b(args, env, cpu),
-          "llama3_8b_stack": lambda: wl_stack(args, env, form, cpu)}[name]
+          "llama3_8b_stack": lambda: wl_stack(args, env, form, cpu),
+          "llama3_8b_attention": lambda: wl_attention(args, env)}[name]
     line = _line(name, args, fn())
     import rotation_post_quantization_b200 as rq
     if rq.respin_device_status() != 0:
