@@ -303,7 +303,8 @@ typedef struct {
  * sequence b; kv_len[b] is its length WITH them, so row cu[b] + i has
  * position kv_len[b] - (cu[b+1] - cu[b]) + i. Token t of a sequence is slot
  * t % page_size of page block_table[b][t / page_size]; entries behind the
- * last used page are not read. Rows from cu[B] on are left as they are.
+ * last used page, and those of pages wholly before an attention window, are
+ * not read. Rows from cu[B] on are left as they are.
  *
  * The arrays are device memory and are checked on the device: a cu or kv_len
  * that does not fit (negative, decreasing, beyond N or the table) or a page id
@@ -315,7 +316,7 @@ typedef struct {
   const int32_t* kv_len;       /* [B] */
   const int32_t* block_table;  /* [B, max_pages] */
   int B;                       /* 0 .. 65536 */
-  int max_pages;
+  int max_pages;               /* max_pages * page_size <= 2^31 - 2^16 */
   int N;                       /* rows; 0 is a no-op */
 } respin_kv_batch_t;
 

@@ -25,8 +25,8 @@ respin_status_t kv_check(const respin_kv_cache_t* c, const respin_kv_batch_t* b,
                 static_cast<long long>(c->num_pages) * c->kv_heads * P);
   if (b->B < 0 || b->N < 0) return fail(RESPIN_ERR_INVALID_ARG, "B=%d and N=%d must not be negative", b->B, b->N);
   if (b->B > 65536) return fail(RESPIN_ERR_UNSUPPORTED, "B=%d: at most 65536 sequences", b->B);
-  if (b->max_pages < 1 || static_cast<long long>(b->max_pages) * P > 0x7FFFFF00LL)
-    return fail(RESPIN_ERR_INVALID_ARG, "max_pages=%d: need at least 1, and max_pages * page_size below 2^31", b->max_pages);
+  if (b->max_pages < 1 || static_cast<long long>(b->max_pages) * P > 0x7FFF0000LL)
+    return fail(RESPIN_ERR_INVALID_ARG, "max_pages=%d: need at least 1, and max_pages * page_size at most 2^31 - 2^16", b->max_pages);
   if (b->N == 0 || b->B == 0) {
     if (b->N != 0) return fail(RESPIN_ERR_INVALID_ARG, "N=%d tokens of no sequence", b->N);
     return ok();
@@ -89,7 +89,7 @@ bool make_tmap_heads(CUtensorMap* m, const void* ptr, int N, int heads, int D, l
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(N)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_heads > 256 ? 256 : box_heads),
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_heads),
                              static_cast<cuuint32_t>(box_tokens)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
@@ -348,7 +348,7 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   a.Hq = q_heads;
   a.G = G;
   a.causal = causal != 0;
-  a.window = window;
+  a.window = window < static_cast<long long>(batch->max_pages) * cache->page_size ? window : 0;   // else it hides nothing
   a.scale = scale * 1.44269504088896340736f;
   a.div_g = G == 1 ? 0ull : ~0ull / static_cast<unsigned long long>(G) + 1ull;
   a.few_rows = most < kKvFewRows ? static_cast<int>(most) : kKvFewRows;
@@ -368,7 +368,7 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
       return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
     const int slot_rows = kTcaSlot / (2 * D);
     CUtensorMap tmQ;
-    if (!make_tmap_heads(&tmQ, q, batch->N, q_heads, D, ld_q, G, slot_rows % G ? 1 : slot_rows / G))
+    if (!make_tmap_heads(&tmQ, q, batch->N, q_heads, D, ld_q, slot_rows % G ? 1 : G, slot_rows % G ? 1 : slot_rows / G))
       return fail(RESPIN_ERR_CUDA, "cuTensorMapEncodeTiled failed for the queries");
     a.plan = const_cast<int4*>(many.plan);
     a.part = const_cast<float*>(many.part);

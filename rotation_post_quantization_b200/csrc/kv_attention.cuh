@@ -165,6 +165,7 @@ struct KvSeq {
   int begin, rows, len;   // first row of the batch, rows * G, length
   int groups;             // row groups of RB rows
   int t0, tiles;          // first tile and tiles of each unit (at least 1 where there are rows)
+  int low;                // first token that any row sees
 };
 
 template <int RB>
@@ -180,8 +181,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvAttnArgs& a, int b) {
   }
   s.groups = (s.rows + RB - 1) / RB;
   const int first = s.len - n;   // position of the first row
-  const int low = a.window > 0 ? max(0, first - a.window + 1) : 0;
-  s.t0 = min(low, s.len) / kKvTile;
+  s.low = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  s.t0 = min(s.low, s.len) / kKvTile;
   s.tiles = max(1, (s.len + kKvTile - 1) / kKvTile - s.t0);
   return s;
 }
@@ -313,7 +314,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         int row = -1;
         KvScale sc = kv_scale_of(0.0f, 0.0f);
         sc.lv = -INFINITY;
-        if (tok < s.len && lane / nsub < n - i0) {
+        if (tok < s.len && tok + SP > s.low && lane / nsub < n - i0) {   // (pages behind the window may be gone)
           const int page = kv_page(a.c, b, tok);
           if (page >= 0) {
             const int ph = page * a.c.H + h;

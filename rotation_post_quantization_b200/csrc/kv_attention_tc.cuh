@@ -193,28 +193,29 @@ __device__ __forceinline__ TcaSeq tca_seq(const KvAttnArgs& a, int b) {
   return s;
 }
 
-// First step and number of steps (at least 1) of row group g.
-__device__ __forceinline__ int2 tca_steps(const KvAttnArgs& a, int n, int len, int rows, int g) {
+// First step and number of steps (at least 1) of row group g, and the first token that one of its rows sees.
+__device__ __forceinline__ int3 tca_steps(const KvAttnArgs& a, int n, int len, int rows, int g) {
   const int first = len - n + kv_div_g(a, g * kTcaGroup);
   const int last = len - n + kv_div_g(a, min(rows, (g + 1) * kTcaGroup) - 1);
   const int hi = a.causal ? min(last, len - 1) : len - 1;
-  if (hi < 0) return make_int2(0, 1);
+  if (hi < 0) return make_int3(0, 1, 0);
   const int lo = a.window > 0 ? min(hi, max(0, first - a.window + 1)) : 0;
   const int t0 = lo / kTcaTile;
-  return make_int2(t0, hi / kTcaTile - t0 + 1);
+  return make_int3(t0, hi / kTcaTile - t0 + 1, lo);
 }
 
 // Where a role stands in the block's piece of the line.
 struct TcaCursor {
   TcaSeq s;
   int b, g, h, z;   // sequence, row group, head, steps of the unit already behind
-  int t0, tiles;    // of the unit
+  int t0, tiles, low;   // of the unit
   int left;
 
   __device__ __forceinline__ void unit(const KvAttnArgs& a) {
-    const int2 t = tca_steps(a, s.n, s.len, s.rows, g);
+    const int3 t = tca_steps(a, s.n, s.len, s.rows, g);
     t0 = t.x;
     tiles = t.y;
+    low = t.z;
   }
   __device__ __forceinline__ int steps() const { return min(left, tiles - z); }
   __device__ __forceinline__ void next(const KvAttnArgs& a) {
@@ -728,7 +729,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             b = ahead.b;
             h = ahead.h;
             t = (ahead.t0 + ahead.z + aj) * kTcaTile + 16 * (lane & 3);
-            if (t >= ahead.s.len) b = -1;
+            const int SP = min(a.c.P, kTcaTile);
+            if (t >= ahead.s.len || (t & ~(SP - 1)) + SP <= ahead.low) b = -1;   // (pages behind the window may be gone)
           }
           if (++aj == ahead.steps()) {
             aj = 0;

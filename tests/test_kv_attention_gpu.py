@@ -191,3 +191,61 @@ def test_max_q_below_the_truth_is_recorded():
     rq.respin_kv_attention(bt.cache, tq, bt.t_len, bt.t_table, out, workspace(bt.cache, 4, 41, 2), cu=bt.t_cu, max_q=2)
     assert rq.respin_device_status() == 512
     assert (out[1:] == 7).all() and not (out[:1] == 7).all()
+
+
+@pytest.mark.parametrize("q", [1, 3, 40])
+@pytest.mark.parametrize("P", [16, 64, 128])
+def test_pages_behind_the_window_may_be_gone(q, P):
+    """A sliding window's freed pages have no id any more: not looked at, nothing recorded."""
+    bt = Batch([q, q], [700, 300], 2, 128, P, seed=14).to_gpu()
+    want = attend(bt, 8, window=100)
+    for b, n in enumerate(bt.kv_lens):
+        gone = max(0, n - q - 100 + 1) // P   # pages that no row's window touches
+        assert gone > 0
+        bt.t_table[b, :gone] = -1
+    got = attend(bt, 8, window=100)
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+@pytest.mark.parametrize("q", [1, 50])
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_scale_negative_or_zero(scale, q):
+    bt = Batch([q], [300], 2, 128, 32, seed=15).to_gpu()
+    attend(bt, 4, scale=scale)
+
+
+@pytest.mark.parametrize("H,G,q", [(1, 16, 1), (1, 17, 1), (1, 64, 3), (2, 32, 9), (1, 5, 300)])
+def test_many_query_heads_of_a_key_head(H, G, q):
+    bt = Batch([q, q], [400, q + 1], H, 64, 64, seed=16).to_gpu()
+    attend(bt, H * G)
+
+
+@pytest.mark.parametrize("q", [2, 60])
+def test_a_row_of_nan_stays_alone(q):
+    bt = Batch([q], [200], 1, 128, 64, seed=17).to_gpu()
+    x = np.random.default_rng(4).standard_normal((q, 4, 128))
+    tq, _ = bf16(x)
+    ws = workspace(bt.cache, 4, q)
+    outs = []
+    for bad in (None, float("nan"), float("inf")):
+        t = tq.clone()
+        if bad is not None:
+            t[1, 2, 5] = bad
+        out = torch.zeros_like(tq)
+        rq.respin_kv_attention(bt.cache, t, bt.t_len, bt.t_table, out, ws)
+        outs.append(out)
+    for o in outs[1:]:
+        assert torch.isnan(o[1, 2]).all()
+        o[1, 2] = outs[0][1, 2]
+        assert torch.equal(o, outs[0])
+
+
+def test_window_beyond_any_length():
+    bt = Batch([40, 1], [30, 500], 1, 64, 16, seed=18).to_gpu()
+    a = attend(bt, 2)
+    for window in (2 ** 31 - 1, 16 * bt.table.shape[1]):
+        q = np.random.default_rng(1).standard_normal((bt.N, 2, 64))
+        out, lse = torch.zeros_like(a[0]), torch.zeros_like(a[1])
+        rq.respin_kv_attention(bt.cache, bf16(q)[0], bt.t_len, bt.t_table, out, workspace(bt.cache, 2, bt.N), cu=bt.t_cu,
+                               window=window, lse=lse)
+        assert torch.equal(out, a[0]) and torch.equal(lse, a[1])
