@@ -193,9 +193,9 @@ respin_status_t respin_qk_norm_rope(const void* q, const void* k, int N, int q_h
   RopeArgs a{static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<bf16*>(q_out), static_cast<bf16*>(k_out),
              static_cast<const bf16*>(q_weight), static_cast<const bf16*>(k_weight), positions, inv_freq,
              ld_q, ld_k, ld_qo, ld_ko, N, q_heads, kv_heads, rot_dim, 1, eps};
-  // Many tokens: as many a block as make one wave of six blocks on each of 148 SMs, at most 8 (their
+  // Many tokens: as many a block as make one wave of five blocks on each of 148 SMs, at most 8 (their
   // sines and cosines are formed once for all heads). Few: one, and its vectors go to several blocks.
-  a.tokens = N < 592 ? 1 : N >= 8 * 888 ? 8 : (N + 887) / 888;
+  a.tokens = N < 592 ? 1 : N >= 8 * 740 ? 8 : (N + 739) / 740;
   const int V = kRopeThreads / (head_dim / 8);
   const int passes = (a.tokens * (q_heads + kv_heads) + V - 1) / V;
   const int y = N >= 592 ? 1 : passes;

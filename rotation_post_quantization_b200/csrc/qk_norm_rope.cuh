@@ -11,10 +11,13 @@
 // whole turns before the fp32 sine and cosine.
 //
 // Memory bound: every element is read and written once (4 bytes an element).
-// A vector of d values is held by d/8 neighbouring lanes, 16 bytes each, so
-// the sum of squares and the partner values of a pair are register shuffles.
-// A block takes kRopeTokens tokens, computes their sines and cosines once
-// for all heads, and keeps kRopeUnroll vectors a lane in flight.
+// A vector of d values is held by d/8 neighbouring lanes, both values of a
+// pair in the same one (two runs of 8 bytes a lane, half the rotated width
+// apart), so only the sum of squares needs shuffles. A block takes several
+// tokens and computes their sines and cosines once for all heads; the next
+// vectors are loaded while the last ones are turned. (With 16 consecutive
+// bytes a lane and the partner fetched by shuffles: 27 us for 4096 tokens of
+// 40 heads.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,7 +58,7 @@ __device__ __forceinline__ float2 rope_cos_sin(int position, float freq) {
 }
 
 template <int D, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 5) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int L = D / 8;                         // lanes of one vector
   constexpr int V = kRopeThreads / L;              // vectors of one pass of the block
   extern __shared__ float2 rope_cs[];              // [tokens][rot / 2]
@@ -68,38 +71,65 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const Rop
 
   grid_dep_wait();
   grid_dep_launch();
-  // A lane reads the angles of its 8 values (4 pairs interleaved): angle E l + i lies at i * (half / E) + l,
-  // so that neighbouring lanes read neighbouring ones.
-  constexpr int E = INTERLEAVED ? 4 : 8;
+  // Lane l turns the angles 4 l .. 4 l + 3; angle 4 l + i lies at i * (half / 4) + l, so that
+  // neighbouring lanes read neighbouring ones.
+  const int turning = half / 4;   // lanes
   for (int i = tid; i < nt * half; i += kRopeThreads) {
     const int t = i / half, f = i - t * half;
-    rope_cs[t * half + (f % E) * (half / E) + f / E] = rope_cos_sin(a.positions[t0 + t], a.inv_freq[f]);
+    rope_cs[t * half + (f & 3) * turning + (f >> 2)] = rope_cos_sin(a.positions[t0 + t], a.inv_freq[f]);
   }
+  // This lane's values: 4 from o0 on and 4 from o1 on (in units of 4).
+  const bool in = li < turning;
+  const int o0 = INTERLEAVED || !in ? 2 * li : li;
+  const int o1 = INTERLEAVED || !in ? 2 * li + 1 : li + turning;
+  auto read8 = [&](const __nv_bfloat16* p) {
+    const uint2 x = reinterpret_cast<const uint2*>(p)[o0], y = reinterpret_cast<const uint2*>(p)[o1];
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
   uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
-  if (a.q_weight != nullptr) wq = reinterpret_cast<const uint4*>(a.q_weight)[li];
-  if (a.k_weight != nullptr) wk = reinterpret_cast<const uint4*>(a.k_weight)[li];
+  if (a.q_weight != nullptr) wq = read8(a.q_weight);
+  if (a.k_weight != nullptr) wk = read8(a.k_weight);
   __syncthreads();
 
   // Blocks of one row of the grid share its tokens: each takes every
   // gridDim.y-th pass of V vectors.
-  for (int base = blockIdx.y * V; base < total; base += gridDim.y * V * kRopeUnroll) {
-    uint4 raw[kRopeUnroll];
-    int vec[kRopeUnroll];
+  const int step = static_cast<int>(gridDim.y) * V;
+  const int dt = step / heads, dh = step - dt * heads;   // a step on
+  uint4 next[kRopeUnroll];
+  int next_t[kRopeUnroll], next_h[kRopeUnroll];   // token (of the block) and head; token nt or more: none
+  int at_t = (static_cast<int>(blockIdx.y) * V + tid / L) / heads;
+  int at_h = static_cast<int>(blockIdx.y) * V + tid / L - at_t * heads;
+  auto load = [&]() {   // the next vectors are on their way while the last ones are turned
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      vec[u] = base + u * static_cast<int>(gridDim.y) * V + tid / L;
-      raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (vec[u] < total) {
-        const int t = vec[u] / heads, h = vec[u] - t * heads;
-        const __nv_bfloat16* p = h < a.Hq ? a.q + (t0 + t) * a.ldq + static_cast<long long>(h) * D
-                                          : a.k + (t0 + t) * a.ldk + static_cast<long long>(h - a.Hq) * D;
-        raw[u] = reinterpret_cast<const uint4*>(p)[li];
+      next_t[u] = at_t;
+      next_h[u] = at_h;
+      next[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (at_t < nt)
+        next[u] = read8(at_h < a.Hq ? a.q + (t0 + at_t) * a.ldq + at_h * D : a.k + (t0 + at_t) * a.ldk + (at_h - a.Hq) * D);
+      at_t += dt;
+      at_h += dh;
+      if (at_h >= heads) {
+        at_h -= heads;
+        ++at_t;
       }
     }
+  };
+  load();
+  for (int base = blockIdx.y * V; base < total; base += step * kRopeUnroll) {
+    uint4 raw[kRopeUnroll];
+    int vt[kRopeUnroll], vh[kRopeUnroll];
 #pragma unroll
     for (int u = 0; u < kRopeUnroll; ++u) {
-      const bool live = vec[u] < total;   // lanes of dead vectors still take part in the shuffles
-      const int t = live ? vec[u] / heads : 0, h = live ? vec[u] - t * heads : 0;
+      raw[u] = next[u];
+      vt[u] = next_t[u];
+      vh[u] = next_h[u];
+    }
+    load();
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      const bool live = vt[u] < nt;   // lanes of absent vectors still take part in the shuffles
+      const int t = live ? vt[u] : 0, h = vh[u];
       const bool is_q = h < a.Hq;
       float x[8], y[8];
       bf16x8_to_f32(raw[u], x);
@@ -135,43 +165,22 @@ __global__ void __launch_bounds__(kRopeThreads, 6) qk_norm_rope_kernel(const Rop
           bf16x8_to_f32(raw[u], x);
         }
       }
-      const float2* cs = rope_cs + t * half;
-      if constexpr (INTERLEAVED) {
+      const float2* cs = rope_cs + t * half + li;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = x[i];
+      if (in) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float2 r = make_float2(1.0f, 0.0f);
-          if (8 * li + 2 * i < a.rot) r = cs[i * (half / 4) + li];
-          y[2 * i] = x[2 * i] * r.x - x[2 * i + 1] * r.y;
-          y[2 * i + 1] = x[2 * i + 1] * r.x + x[2 * i] * r.y;
-        }
-        if (8 * li >= a.rot) {   // a rotation by nothing, without its 0 * inf
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i];
-        }
-      } else {
-        const int hl = half / 8;   // lanes of half the rotated values
-        const bool first = li < hl, in = li < 2 * hl;
-        const int lane = tid & 31;
-        const int src = (lane & ~(L - 1)) + (in ? (first ? li + hl : li - hl) : li);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xFFFFFFFFu, x[i], src);
-        if (in) {
-          const float2* c = cs + (first ? li : li - hl);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 r = c[i * hl];
-            y[i] = first ? x[i] * r.x - y[i] * r.y : x[i] * r.x + y[i] * r.y;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i];
+          const float2 r = cs[i * turning];
+          const int p = INTERLEAVED ? 2 * i : i, q = INTERLEAVED ? 2 * i + 1 : i + 4;
+          y[p] = x[p] * r.x - x[q] * r.y;
+          y[q] = x[q] * r.x + x[p] * r.y;
         }
       }
       if (live) {
-        __nv_bfloat16* p = is_q ? a.q_out + (t0 + t) * a.ldqo + static_cast<long long>(h) * D
-                                : a.k_out + (t0 + t) * a.ldko + static_cast<long long>(h - a.Hq) * D;
-        reinterpret_cast<uint4*>(p)[li] = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                     pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        __nv_bfloat16* p = is_q ? a.q_out + (t0 + t) * a.ldqo + h * D : a.k_out + (t0 + t) * a.ldko + (h - a.Hq) * D;
+        reinterpret_cast<uint2*>(p)[o0] = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+        reinterpret_cast<uint2*>(p)[o1] = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
       }
     }
   }
