@@ -266,7 +266,7 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache, const respin_kv_b
   a.ldk = ld_k;
   a.ldv = ld_v;
   // 32 rows a block share the lookups; 8 where that leaves SMs without a block. A block takes as many
-  // heads as make 1024 pieces of 16 bytes (8 a thread): more of them hide one another's lookups.
+  // heads as make 2048 pieces of 8 bytes (16 a thread): more of them hide one another's lookups.
   const bool few = batch->N < 32 * 148;
   const void* fn = cache->head_dim == 64 ? (few ? reinterpret_cast<const void*>(&kv_read_kernel<64, 8>)
                                                 : reinterpret_cast<const void*>(&kv_read_kernel<64, 32>))

@@ -277,12 +277,12 @@ constexpr int kKvReadThreads = 128;
 
 // grid (chunks of R rows, K | V, groups of heads). One search finds the first row's sequence;
 // each row's lane walks on from there and looks its page up, so the rows'
-// lookups run side by side. Then the block walks heads, rows and 16-byte
-// pieces of codes: neighbouring rows of a page are neighbours in memory, so a
+// lookups run side by side. Then the block walks heads, rows and 8-byte
+// pieces of codes (16 bytes out, so a warp's stores are whole lines): neighbouring rows of a page are neighbours in memory, so a
 // head's rows are one run of codes.
 template <int D, int R>
 __global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArgs a) {
-  constexpr int L = D / 16;   // 16-byte pieces of a token's codes
+  constexpr int L = D / 8;   // 8-byte pieces of a token's codes
   __shared__ int page_of[R], slot_of[R];
   const KvView& c = a.c;
   const int tid = threadIdx.x;
@@ -323,19 +323,19 @@ __global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArg
   // this block's heads
   const int h0 = blockIdx.z * a.heads, nh = min(a.heads, c.H - h0);
   const int total = nh * R * L;
-  constexpr int U = 4;   // pieces of a thread in flight
+  constexpr int U = 8;   // pieces of a thread in flight
   for (int p0 = tid; p0 < total; p0 += U * kKvReadThreads) {
-    uint4 w[U];
+    uint2 w[U];
     float s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int p = p0 + u * kKvReadThreads;
       const int row = (p / L) % R, h = h0 + p / (L * R);
-      w[u] = make_uint4(0u, 0u, 0u, 0u);
+      w[u] = make_uint2(0u, 0u);
       s[u] = 0.0f;
       if (p < total && page_of[row] >= 0) {
         const long long ph = static_cast<long long>(page_of[row]) * c.H + h;
-        w[u] = reinterpret_cast<const uint4*>(codes + (ph * c.P + slot_of[row]) * D)[p % L];
+        w[u] = reinterpret_cast<const uint2*>(codes + (ph * c.P + slot_of[row]) * D)[p % L];
         s[u] = scales[ph];
       }
     }
@@ -344,19 +344,17 @@ __global__ void __launch_bounds__(kKvReadThreads) kv_read_kernel(const KvReadArg
       const int p = p0 + u * kKvReadThreads;
       const int row = (p / L) % R, h = h0 + p / (L * R);
       if (p >= total || page_of[row] < 0) continue;
-      const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
-      uint32_t o[8];
+      const uint32_t in[2] = {w[u].x, w[u].y};
+      uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {   // (a bit trick in place of the conversion took more registers: 34 us against 30)
+      for (int i = 0; i < 2; ++i) {   // (a bit trick in place of the conversion took more registers: 34 us against 30)
         float x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(in[i] >> (8 * j))), s[u]);
         o[2 * i] = pack_bf16x2(x[0], x[1]);
         o[2 * i + 1] = pack_bf16x2(x[2], x[3]);
       }
-      uint4* to = reinterpret_cast<uint4*>(out + (r0 + row) * ld + static_cast<long long>(h) * D) + 2 * (p % L);
-      to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      reinterpret_cast<uint4*>(out + (r0 + row) * ld + static_cast<long long>(h) * D)[p % L] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
