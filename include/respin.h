@@ -12,14 +12,16 @@
  *      (zh §2.1-§2.2; nl §2B-§2C; fr §2B-§2C), fused with
  *   2. per-token symmetric INT4 quantization of h' (W4A4, zh §3-§4), and
  *   3. the W4A4 GEMM that consumes those codes (zh §2.2: the linears stay
- *      ordinary linears once the rotations are fused into their weights).
+ *      ordinary linears once the rotations are fused into their weights), and
+ *   4. the attention half of a layer between those linears: head norms and
+ *      position rotation, an 8-bit key/value cache, attention over it.
  *
  * Conventions for every call:
  *   - Tokens are rows; tensors are row-major and contiguous.
  *   - bf16 means IEEE bfloat16 (raw 16-bit storage), fp32 means IEEE binary32.
  *   - INT4 codes are packed two per byte: element 2j in the low nibble of byte
  *     j, element 2j+1 in the high nibble, two's complement (value & 0xF).
- *   - All tensor pointers are DEVICE pointers owned by the caller, on the
+ *   - All tensor pointers (those inside structs too) are DEVICE pointers owned by the caller, on the
  *     device that is current when the call is made, 16-byte aligned unless
  *     stated otherwise. The library never allocates per call.
  *   - `stream` is a cudaStream_t handle (NULL = legacy default stream). Calls
