@@ -29,7 +29,10 @@
 // leaves (M, l, O) in the workspace; kv_combine_kernel joins those.
 //
 // Bound: the cache's bytes. Four consumer warps and a producer warp (tensor
-// copies through a ring of kKvStages tiles of 2 * 64 * D bytes).
+// copies through a ring of kKvStages tiles of 2 * 64 * D bytes), three blocks
+// an SM (two with four stages: 75 us where three take 66). 64 sequences of 32
+// query heads over 8 at 4096 tokens: 97 us, 5.5 TB/s with the join; two of 64
+// over 8 at 131071: 90 us, 5.9 TB/s, and 9 us for the join of 28 pieces a unit.
 #pragma once
 
 #include <cuda.h>

@@ -32,11 +32,14 @@
 // before; the weights' own maximum (of the packed fp16) says whether they must
 // be formed again.
 //
-// Bound. A step of 64 tokens takes 2450 cycles for both tiles (D = 128). The
-// tensor core's share is 1024 of them, the exponentials' 1024, and shared
-// memory's 1536: Q 64 KB (read anew for every 64 tokens), K and V 64 KB,
-// codes in, out and widened 64 KB, at 128 bytes a cycle. Sixteen warps for
-// the rows (half a row a thread, the maxima exchanged) took 3000 cycles.
+// Bound. A step of 64 tokens takes 2450 cycles for both tiles at D = 128, 1900
+// for one alone. The tensor core's share is 1024 of them, the exponentials'
+// 1024, shared memory's 1536 (Q 64 KB, read anew for every 64 tokens, K and V
+// 64 KB, codes in, out and widened 64 KB, at 128 bytes a cycle). With half of
+// Q's reads or the widening left out a step is 5 % shorter, without the
+// exponentials 15 %: the rest is a row warp's own chain of waits and tensor
+// memory reads and writes, about 1000 cycles beside the weights. Sixteen warps
+// for the rows (half a row a thread, the maxima exchanged) took 3000 cycles.
 // Two 4096-token prompts, 32 query heads over 8: 500 us, 550 TFLOP/s.
 //
 // Tensor memory: S0, S1 (64 columns each), P0, P1 (2 x 32 each), O0, O1 (D
