@@ -359,14 +359,15 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache,
  *     s_j = scale * (q . k_j),  j < n
  *           and j <= p (causal)  and j > p - window (window > 0)
  *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
- * A row that sees no token gets out 0 and lse -inf. Products are exact and
+ * No input may overlap an output. A row that sees no token gets out 0 and lse -inf. Products are exact and
  * sums fp32; the weights are rounded to fp16 before the second product and
  * the output to bf16.
  *
  *   q         : bf16 [N, q_heads, head_dim] (stride ld_q).
  *   q_heads   : a multiple of kv_heads, at most 1024.
  *   max_q     : at least the most rows of a sequence, 0 if unknown (a value
- *               below the truth may leave longer sequences out: 512).
+ *               below the truth may leave longer sequences out: 512). Without
+ *               cu it is N / B, whatever is given.
  *   causal    : 0 or 1; window: 0 (none) or the last tokens a row sees, its
  *               own among them (needs causal).
  *   out       : bf16 [N, q_heads, head_dim] (stride ld_out).

@@ -315,6 +315,10 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   if (window > 0 && !causal) return fail(RESPIN_ERR_INVALID_ARG, "a window needs causal");
   if (!(scale > -1e30f && scale < 1e30f)) return fail(RESPIN_ERR_INVALID_ARG, "scale must be finite (below 1e30)");
   if (batch->N == 0) return ok();
+  if (static_cast<long long>(batch->N) * (q_heads / H) > 0x7FFFFFFFLL)
+    return fail(RESPIN_ERR_UNSUPPORTED, "N * q_heads / kv_heads = %lld rows: at most 2^31 - 1",
+                static_cast<long long>(batch->N) * (q_heads / H));
+  if (batch->cu == nullptr) max_q = batch->N / batch->B;   // what it is, whatever was given
   if (q == nullptr || out == nullptr || workspace == nullptr)
     return fail(RESPIN_ERR_INVALID_ARG, "q, out and workspace must be non-NULL");
   const long long row = static_cast<long long>(q_heads) * D;

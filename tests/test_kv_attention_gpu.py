@@ -249,3 +249,17 @@ def test_window_beyond_any_length():
         rq.respin_kv_attention(bt.cache, bf16(q)[0], bt.t_len, bt.t_table, out, workspace(bt.cache, 2, bt.N), cu=bt.t_cu,
                                window=window, lse=lse)
         assert torch.equal(out, a[0]) and torch.equal(lse, a[1])
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_c_call_without_cu_and_max_q(q):
+    """N / B rows each and no max_q: as if it had been given."""
+    bt = Batch([q, q], [100, 77], 1, 128, 32, seed=19).to_gpu()
+    want, _ = attend(bt, 4)
+    tq, _ = bf16(np.random.default_rng(1).standard_normal((2 * q, 4, 128)))
+    c, b, _ = rq._kv_args(bt.cache, 2 * q, bt.t_len, bt.t_table, None)
+    out, ws = torch.zeros_like(tq), workspace(bt.cache, 4, 2 * q)
+    rq._check(rq.lib.respin_kv_attention(c, b, tq.data_ptr(), 4, 512, 0, 1, 0, 128 ** -0.5, out.data_ptr(), 512, None,
+                                         ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    assert rq.respin_device_status() == 0 and torch.equal(out, want)

@@ -81,6 +81,11 @@ def test_norm_rope_arguments(kw, want):
     assert rq.lib.respin_qk_norm_rope(*f.values(), None) == want and rq.last_error()
 
 
+def test_attention_rows_beyond_32_bits():
+    b = batch(N=1 << 30, B=1 << 10)
+    assert attention(b=b, q_heads=8, ld_q=512, ld_out=512) == rq.RESPIN_ERR_UNSUPPORTED
+
+
 def test_empty_calls_do_nothing():
     b = batch(N=0, B=0, kv_len=None, block_table=None)
     assert rq.lib.respin_kv_append(cache(), b, None, None, 0, 0, None) == rq.RESPIN_OK
