@@ -40,7 +40,7 @@
 // exponentials 15 %: the rest is a row warp's own chain of waits and tensor
 // memory reads and writes, about 1000 cycles beside the weights. Sixteen warps
 // for the rows (half a row a thread, the maxima exchanged) took 3000 cycles.
-// Two 4096-token prompts, 32 query heads over 8: 500 us, 550 TFLOP/s.
+// Two 4096-token prompts, 32 query heads over 8: 380 us, 723 TFLOP/s.
 //
 // Tensor memory: S0, S1 (64 columns each), P0, P1 (2 x 32 each), O0, O1 (D
 // each). Shared memory at D = 128: Q 64 KB, K 32 KB, V 48 KB, ring 64 KB.
@@ -62,10 +62,12 @@ constexpr int kTcaThreads = 20 * 32;
 constexpr int kTcaRegsRows = 144, kTcaRegsCodes = 56, kTcaRegsLast = 80;
 constexpr int kTcaVStages = 3;
 constexpr int kTcaMinTiles = 8;     // least piece of a block
-// A unit's queries, first step and output cost about as much as three steps;
+// A unit's queries, first step and output cost about as much as six steps;
 // the line of work counts them, so that blocks of many short units (a causal
-// prompt's first rows) get fewer of their steps.
-constexpr int kTcaUnitCost = 3;
+// prompt's first rows) get fewer of their steps. Two 4096-token prompts, at a
+// cost of 3, 5, 6, 7, 10: 428, 387, 380, 384, 394 us.
+constexpr int kTcaUnitCost = 6;
+static_assert(kTcaMinTiles > kTcaUnitCost, "a piece has a step");
 constexpr int kTcaMaxBlocks = 160;  // one per SM
 constexpr int kTcaMeta = 16;        // steps whose scales are kept (the ring is at most eight ahead of the rows)
 constexpr int kTcaSlots = 8;        // of the ring
@@ -674,29 +676,38 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         for (int r0 = 0; r0 < kTcaRows; r0 += RE) {
           const uint8_t* from = take();
           if (!ok) break;
-          const int li = pt % L;
+          // TR threads a row, four pieces each: piece (i + row) % 4 * TR + c, so that the rows of eight
+          // neighbouring lanes lie on different banks, read and written
+          constexpr int TR = L / 4;
+          const int r = r0 + pt / TR, c = pt % TR;
+          uint4 w[4];
+          uint32_t m2 = 0;
 #pragma unroll
-          for (int i = 0; i < RE * L / 128; ++i) {
-            const int r = r0 + pt / L + 128 / L * i;
-            const uint4 w = reinterpret_cast<const uint4*>(from)[pt + 128 * i];
-            // (a row with an infinity or NaN is scaled as one of 2^127: its results are not finite anyway)
-            uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-            m = max(m & 0xFFFFu, m >> 16);
+          for (int i = 0; i < 4; ++i) {
+            w[i] = reinterpret_cast<const uint4*>(from)[pt / TR * L + ((i + r) & 3) * TR + c];
+            m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[i].x & 0x7FFF7FFFu, w[i].y & 0x7FFF7FFFu),
+                                       __vmaxu2(w[i].z & 0x7FFF7FFFu, w[i].w & 0x7FFF7FFFu)));
+          }
+          uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const int e = max(-110, min(127, static_cast<int>(m >> 7) - 127));
-            // a negative scale goes with the queries, so that the factors are not negative
-            const float up = copysignf(__int_as_float((14 - e + 127) << 23), a.scale);
+          for (int o = TR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+          // (a row with an infinity or NaN is scaled as one of 2^127: its results are not finite anyway)
+          const int e = max(-110, min(127, static_cast<int>(m >> 7) - 127));
+          // a negative scale goes with the queries, so that the factors are not negative
+          const float up = copysignf(__int_as_float((14 - e + 127) << 23), a.scale);
+          uint8_t* qs = smem + C::OQ + tile * C::OpQ + (r >> 3) * 1024 + (r & 7) * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int piece = ((i + r) & 3) * TR + c;
             float f[8];
-            bf16x8_to_f32(w, f);
-            *reinterpret_cast<uint4*>(smem + C::OQ + tile * C::OpQ + (li >> 3) * BlockQ + (r >> 3) * 1024 + (r & 7) * 128 +
-                                      (((li & 7) ^ (r & 7)) << 4)) =
+            bf16x8_to_f32(w[i], f);
+            *reinterpret_cast<uint4*>(qs + (piece >> 3) * BlockQ + (((piece & 7) ^ (r & 7)) << 4)) =
                 make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
                            pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
-            if (li == 0)
-              reinterpret_cast<float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r] =
-                  __int_as_float((e - 14 + 127) << 23) * fabsf(a.scale);
           }
+          if (c == 0)
+            reinterpret_cast<float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r] =
+                __int_as_float((e - 14 + 127) << 23) * fabsf(a.scale);
           give(r0 + RE >= kTcaRows ? qfull + 8 * tile : 0u);
         }
       }

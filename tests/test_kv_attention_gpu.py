@@ -155,7 +155,9 @@ def test_repeated_and_on_streams():
 @pytest.mark.parametrize("q", [1, 50])
 def test_refused_indexes_are_recorded(q):
     """A page id outside the cache leaves its tokens out; a length beyond the
-    table, or a cu that does not fit, leaves the sequence out. Nothing else changes."""
+    table, or a cu that does not fit, leaves the sequence out: the other's rows are those of a
+    batch without it (to the bit: the same line of work; beside a sequence that counts, the
+    order of a shared unit's sums may be another)."""
     bt = Batch([q, q], [200, 200], 1, 128, 64, seed=12).to_gpu()
     tq, _ = bf16(np.random.default_rng(3).standard_normal((2 * q, 4, 128)))
     ws = workspace(bt.cache, 4, 2 * q)
@@ -174,12 +176,16 @@ def test_refused_indexes_are_recorded(q):
         assert rq.respin_device_status() == 511
         assert torch.equal(got[q:], good[q:]) and not torch.isnan(got).any()
         bt.t_table.copy_(keep)
+    bt.t_cu[0] = q   # no rows of the first sequence
+    alone = call()
+    assert rq.respin_device_status() == 0 and (alone[:q] == 7).all()
+    bt.t_cu[0] = 0
     for t, i, bad in ((bt.t_len, 0, 10 ** 6), (bt.t_len, 0, -1), (bt.t_cu, 0, -3), (bt.t_cu, 0, 2 * q + 9)):
         keep = t.clone()
         t[i] = bad
         got = call()
         assert rq.respin_device_status() == 512
-        assert torch.equal(got[q:], good[q:]) and (got[:q] == 7).all()
+        assert torch.equal(got[q:], alone[q:]) and (got[:q] == 7).all()
         t.copy_(keep)
     assert torch.equal(call(), good)
     assert rq.respin_device_status() == 0
