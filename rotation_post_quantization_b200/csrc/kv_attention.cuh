@@ -8,11 +8,11 @@
 // amax. The products of the tensor cores are then exact and summed in fp32,
 // and the page's scale is applied to the sum. The weights of a page carry
 // its v scale: p_j = 2^(s_j log2 e + log2 vs - M), M a running maximum of
-// that exponent, so p <= 2^14 fits fp16 and the accumulators need no scale of
+// that exponent, so p <= 2^15 fits fp16 and the accumulators need no scale of
 // their own; the sum l = sum p_j / vs takes them in fp32 before the rounding.
 // Rounding p to fp16 is the one loss: half a step is 2^-12 of each weight
-// down to 2^-20 of the largest (bf16 would lose 2^-9), beside the 2^-9 of the
-// bf16 output.
+// down to 2^-16 of the largest, and 2^-27 of the largest below (bf16 would
+// lose 2^-9), beside the 2^-9 of the bf16 output.
 //
 // Layout. A warp takes 16 tokens of a 64-token tile and 8 rows at a time with
 // the transposed products S^T = K Q^T and O^T = V^T P^T: with at most 8 rows
@@ -53,8 +53,8 @@ constexpr int kKvMaxBlocks = 592;    // 4 per SM
 constexpr int kKvMinTiles = 4;       // least piece of a block
 constexpr int kKvFewRows = 16;       // rows a key head up to which a sequence is this kernel's
 constexpr int kKvPlan = 3;           // int4s a block leaves about its piece (KvJoin)
-constexpr float kKvBias = 6.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^14 in fp16
-constexpr float kKvLazy = 8.0f;      // the running maximum may lag by 2^8
+constexpr float kKvBias = 2.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^15 in fp16
+constexpr float kKvLazy = 13.0f;     // the running maximum may lag by 2^13
 
 struct KvAttnArgs {
   KvView c;

@@ -24,7 +24,7 @@
 // their exponentials follow one another. (With 128-token steps S and P do not
 // both fit beside O at D = 128; P in the place of S makes each step a chain of
 // weights, product, scores: measured 5700 cycles for 128 tokens.) The running
-// maximum may lag by 2^8 before the accumulators are rescaled, so rescaling is
+// maximum may lag by 2^13 before the accumulators are rescaled, so rescaling is
 // rare after the first steps and is done by the row's own thread.
 //
 // A row's 64 scores stay in registers: one read of tensor memory, one
@@ -487,7 +487,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 if (32 * c + i < first || 32 * c + i > last) v[c][i] = 0xFF800000u;   // -inf
           }
           // ---- weights against the maximum of the steps before, their sum and their own maximum: the
-          // comparisons run beside the exponentials. Where an exponent passes M by 2^14 (the unit's
+          // comparisons run beside the exponentials. Where an exponent passes M by 2^15 (the unit's
           // first step, and rarely later) the maximum moves and the weights are formed again.
           float ls = 0.0f;
 #pragma unroll 1
@@ -551,9 +551,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
               // the next step's S, looked at where the answer is not waited for
               if (c == 0) there = j + 1 < n && mbar_test_wait(sfull + 8 * tile, (use + 1) & 1);
             }
-            // (after the maximum has moved no weight passes 2^14)
+            // (after the maximum has moved no weight passes 2^15)
             const __half2 tt = __hmax2(top[0], top[1]);
-            const float limit = 16384.0f;   // 2^(kKvBias + kKvLazy)
+            const float limit = 32768.0f;   // 2^(kKvBias + kKvLazy)
             there = __all_sync(0xFFFFFFFFu, there);
             again = !again && __any_sync(0xFFFFFFFFu, unseen || __low2float(tt) > limit || __high2float(tt) > limit);
             if (!again) break;

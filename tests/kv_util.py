@@ -57,8 +57,8 @@ def attend(bt, Hq, *, causal=True, window=0, scale=None, use_cu=True, max_q="max
     2^-8 of itself; each weight's fp16 rounding 2^-11 of its part of
     sum w |v|; its fp32 exponent, of size up to 2^8, 2^-16 (16 half steps of
     2^-24 at 2^8 is 2^-12 in the worst case, reached only by weights of 2^-8
-    of the row's sum: 2^-16 beside the row); fp16's floor, 2^-25 beside a
-    largest weight of 2^6 at least, for every token: n 2^-31 of the largest."""
+    of the row's sum: 2^-16 beside the row); fp16's floor, 2^-25 (half of
+    its smallest step) beside a largest weight of 2^2 at least, for every token: n 2^-27 of the largest."""
     g = np.random.default_rng(seed)
     d = bt.d
     scale = d ** -0.5 if scale is None else scale
@@ -79,7 +79,7 @@ def attend(bt, Hq, *, causal=True, window=0, scale=None, use_cu=True, max_q="max
     got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
     assert (got[n:] == 7).all() and (gl[n:] == 7).all()      # rows behind the last sequence
     got, gl = got[:n], gl[:n]
-    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -16) * spread + max(bt.kv_lens) * 2.0 ** -31 * top[..., None]
+    tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -16) * spread + max(bt.kv_lens) * 2.0 ** -27 * top[..., None]
     bad = ~(np.abs(got - ref) <= tol)
     assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], ref[bad][:5], bad.mean())
     empty = np.isinf(rl)
