@@ -311,7 +311,8 @@ typedef struct {
  * The arrays are device memory and are checked on the device: a cu or kv_len
  * that does not fit (negative, decreasing, beyond N or the table) or a page id
  * outside the cache is recorded (respin_device_status: 512, 511) and its
- * tokens are left out; nothing outside the given buffers is touched.
+ * tokens are left out; nothing outside the given buffers is touched. The
+ * length of a sequence without rows is not looked at.
  */
 typedef struct {
   const int32_t* cu;           /* [B + 1], or NULL: N / B rows each */

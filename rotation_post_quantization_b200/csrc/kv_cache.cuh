@@ -50,6 +50,7 @@ __device__ __forceinline__ bool kv_rows(const KvView& c, int b, int& begin, int&
   begin = c.cu ? c.cu[b] : b * c.per;
   end = c.cu ? c.cu[b + 1] : begin + c.per;
   len = c.kv_len[b];
+  if (begin == end) len = 0;   // no rows (a padded batch): its length is not looked at
   const bool ok = begin >= 0 && begin <= end && end <= c.N && len >= 0 &&
                   static_cast<long long>(len) <= static_cast<long long>(c.max_pages) * c.P;
   if (!ok) {

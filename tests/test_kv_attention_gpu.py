@@ -269,3 +269,17 @@ def test_c_call_without_cu_and_max_q(q):
                                          ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream))
     torch.cuda.synchronize()
     assert rq.respin_device_status() == 0 and torch.equal(out, want)
+
+
+def test_padded_batch():
+    """Sequences without rows, as a graph of a fixed batch size pads with: whatever their length and pages say."""
+    bt = Batch([1, 40, 0, 0], [100, 77, 5, 5], 1, 128, 32, seed=20).to_gpu()
+    a = attend(bt, 4)
+    bt.t_len[2:] = torch.tensor([-7, 10 ** 9], dtype=torch.int32)
+    bt.t_table[2:] = -1
+    b = attend(bt, 4)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    k = torch.zeros(41, 1, 128, dtype=torch.bfloat16, device=DEV)
+    rq.respin_kv_append(bt.cache, k, k, bt.t_len, bt.t_table, cu=bt.t_cu)
+    rq.respin_kv_read(bt.cache, k, k.clone(), bt.t_len, bt.t_table, cu=bt.t_cu)
+    assert rq.respin_device_status() == 0
