@@ -1122,7 +1122,8 @@ def wl_attention(args, env) -> dict:
         table = torch.randperm(B * pages, generator=env.g, device=dev).to(torch.int32).view(B, pages)
         kv_len = torch.full((B,), kv, dtype=torch.int32, device=dev)
         pos = (kv - q + torch.arange(q, device=dev, dtype=torch.int32)).repeat(B)
-        qa, sa = env.codes(N, D), torch.rand(N, generator=env.g, device=dev) + 0.5
+        # heads of a size that gives logits a standard deviation near 2
+        qa, sa = env.codes(N, D), 0.7 * (torch.rand(N, generator=env.g, device=dev) + 0.5)
         qkv = torch.empty(N, (H + 2 * Hk) * d, dtype=torch.bfloat16, device=dev)
         qh, kh, vh = (qkv[:, a * d:b * d].view(N, b - a, d) for a, b in ((0, H), (H, H + Hk), (H + Hk, H + 2 * Hk)))
         at = torch.empty(N, H, d, dtype=torch.bfloat16, device=dev)
