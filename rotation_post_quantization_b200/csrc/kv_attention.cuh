@@ -121,11 +121,6 @@ __device__ __forceinline__ uint32_t codes_pair_f16x2(uint32_t a, uint32_t b) {
   return unbias_f16x2((y & 0x00FF00FFu) ^ 0x64806480u);
 }
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));

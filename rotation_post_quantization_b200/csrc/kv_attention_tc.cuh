@@ -873,7 +873,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4; ++k)   // (kind::f16; the descriptor says fp16)
             tc_mma_bf16(ts, dq + kb * (BlockQ >> 4) + 2 * k, dks + kb * (Block >> 4) + 2 * k, is, kb + k > 0);
         mbar_arrive(sfull + 8 * tile);
         tc_commit(sfull + 8 * tile);
