@@ -8,17 +8,20 @@
 // tiles, and walks the cache in 64-token steps:
 //   warps 0-3, 4-7   one row a thread of tile 0 / 1: S from tensor memory,
 //                    maximum, weights back to tensor memory as fp16;
-//   warps 8-11, 12-15 queries of tile 0 and K / of tile 1 and V from a ring of
-//                    8 KB slots to fp16 operand tiles (128-byte swizzle; two of
-//                    K, three of V);
+//   warps 8-11, 12-15 queries of tile 0 and K / of tile 1 and V, each half from
+//                    a ring of its own of 8 KB slots, to fp16 operand tiles
+//                    (128-byte swizzle; two of K, three of V);
 //   warps 16, 18     one thread each issues a tile's S = Q K^T (both from
 //                    shared memory) and O += P V (P from tensor memory, V with
 //                    its dims contiguous, i.e. N-major);
-//   warp 17          fills the ring: looks up page ids and scales of eight
+//   warp 17          fills the rings: looks up page ids and scales of eight
 //                    steps at a time, copies pages and queries with tensor
 //                    copies (queries with asynchronous ones where a slot's rows
-//                    are no whole tokens), as far ahead as the ring is deep,
-//                    across units.
+//                    are no whole tokens), as far ahead as the rings are deep,
+//                    across units. (A parity wait knows only the phase before,
+//                    so whoever waits on a slot has to take all that it holds:
+//                    a ring that both halves share, each leaving out the other's
+//                    entries, lets one pass a slot whose copy is on its way.)
 // S of the next step is issued as soon as a tile's rows have read theirs, and
 // P has two places of its own, so the rows never wait for the tensor core:
 // their exponentials follow one another. (With 128-token steps S and P do not
@@ -71,8 +74,8 @@ constexpr int kTcaMinTiles = 8;     // least piece of a block
 constexpr int kTcaUnitCost = 6;
 static_assert(kTcaMinTiles > kTcaUnitCost, "a piece has a step");
 constexpr int kTcaMaxBlocks = 160;  // one per SM
-constexpr int kTcaMeta = 16;        // steps whose scales are kept (the ring is at most eight ahead of the rows)
-constexpr int kTcaSlots = 8;        // of the ring
+constexpr int kTcaMeta = 16;        // steps whose scales are kept (the rings are at most eight ahead of the rows)
+constexpr int kTcaSlots = 4;        // of a ring
 constexpr int kTcaSlot = 8192;
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
@@ -346,10 +349,10 @@ template <int D>
 struct TcaCfg {
   static constexpr int OpQ = kTcaRows * D * 2, Op = kTcaTile * D * 2;   // bytes of the fp16 operand tiles
   static constexpr int OQ = 0, OK = 2 * OpQ, OV = OK + 2 * Op, ORing = OV + kTcaVStages * Op;
-  static constexpr int OMeta = ORing + kTcaSlots * kTcaSlot;            // [steps][4] scales of 16 tokens each
+  static constexpr int OMeta = ORing + 2 * kTcaSlots * kTcaSlot;        // [steps][4] scales of 16 tokens each
   static constexpr int OCoef = OMeta + kTcaMeta * 4 * 16;               // [2][256] the rows' factors, by unit parity
   static constexpr int OBar = OCoef + 2 * kTcaGroup * 4;
-  static constexpr int Bars = 21 + 2 * kTcaVStages + 2 * kTcaSlots;
+  static constexpr int Bars = 21 + 2 * kTcaVStages + 4 * kTcaSlots;
   static constexpr int Smem = 1024 + OBar + 8 * Bars + 64;
   static constexpr int Columns = 512;
   static constexpr int SlotFloats = kTcaGroup * (D + 2);
@@ -373,7 +376,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   const uint32_t qfull = bars + 32, qempty = bars + 48, sfull = bars + 64, sfree = bars + 80;   // [2] tiles
   const uint32_t pfull = bars + 96, pfree = bars + 128, drained = bars + 160;                // [2 tiles][2 places of P]
   const uint32_t vfull = bars + 168, vempty = vfull + 8 * kTcaVStages;                       // stages of V
-  const uint32_t efull = vempty + 8 * kTcaVStages, eempty = efull + 8 * kTcaSlots;           // slots
+  const uint32_t efull = vempty + 8 * kTcaVStages, eempty = efull + 16 * kTcaSlots;          // [2 rings] slots
   volatile int* sh = reinterpret_cast<volatile int*>(smem + C::OBar + 8 * C::Bars);
   const uint32_t tslot = base + C::OBar + 8 * C::Bars + 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -395,7 +398,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       mbar_init(vfull + 8 * i, 4);
       mbar_init(vempty + 8 * i, 2);
     }
-    for (int i = 0; i < kTcaSlots; ++i) {
+    for (int i = 0; i < 2 * kTcaSlots; ++i) {
       mbar_init(efull + 8 * i, 32);   // every lane of warp 17, and the bytes of its tensor copies
       mbar_init(eempty + 8 * i, 4);
     }
@@ -626,26 +629,24 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     bool ok = true;
     int seg = 0, slot = 0, ph_e = 0, ph_q = 1, stage = 0, ph_s = 1;
     const int stages = half ? kTcaVStages : 2;
-    auto skip = [&](int n) {   // entries of the other half
-      slot += n;
-      while (slot >= kTcaSlots) {
-        slot -= kTcaSlots;
-        ph_e ^= 1;
-      }
-    };
+    const uint32_t full_e = efull + 8 * kTcaSlots * half, empty_e = eempty + 8 * kTcaSlots * half;   // this half's ring
+    const uint8_t* const ring = smem + C::ORing + half * kTcaSlots * kTcaSlot;
     auto take = [&]() {
-      ok = ok && mbar_wait_warp(efull + 8 * slot, ph_e, kSiteKvLoad);
-      return smem + C::ORing + slot * kTcaSlot;
+      ok = ok && mbar_wait_warp(full_e + 8 * slot, ph_e, kSiteKvLoad);
+      return ring + slot * kTcaSlot;
     };
     // the operand tile is written (and the slot's bytes are read): for the async proxy, then the next user
     auto give = [&](uint32_t full) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(eempty + 8 * slot);
+        mbar_arrive(empty_e + 8 * slot);
         if (full) mbar_arrive(full);
       }
-      skip(1);
+      if (++slot == kTcaSlots) {
+        slot = 0;
+        ph_e ^= 1;
+      }
     };
     auto widen = [&](uint8_t* to, const uint8_t* from) {
       constexpr int Pieces = D / 16;                 // 16-byte pieces of a token's codes
@@ -668,9 +669,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       const int n = cur.steps();
       // ---- queries: scaled by a power of two to fp16
       constexpr int L = D / 8, RE = kTcaSlot / (2 * D);   // pieces of a row, rows of a slot
-      constexpr int Entries = kTcaRows / RE;   // of a tile
       const int tile = half, row0 = cur.g * kTcaGroup;
-      if (half == 1) skip(Entries);
       if (row0 + tile * kTcaRows < cur.s.rows) {
         ok = mbar_wait_warp(qempty + 8 * tile, ph_q, kSiteKvFree);
         ph_q ^= 1;
@@ -713,18 +712,15 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           give(r0 + RE >= kTcaRows ? qfull + 8 * tile : 0u);
         }
       }
-      if (half == 0 && row0 + kTcaRows < cur.s.rows) skip(Entries);
       // ---- codes
 #pragma unroll 1
       for (int j = 0; j < n && ok; ++j) {
-        if (half == 1) skip(1);
         const uint8_t* from = take();
         const uint32_t full = (half ? vfull : kfull) + 8 * stage, empty = (half ? vempty : kempty) + 8 * stage;
         ok = ok && mbar_wait_warp(empty, ph_s, kSiteKvFree);
         if (!ok) break;
         widen(smem + (half ? C::OV : C::OK) + stage * C::Op, from);
         give(full);
-        if (half == 0) skip(1);
         if (++stage == stages) {
           stage = 0;
           ph_s ^= 1;
@@ -736,15 +732,15 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
   } else {
     regs_give<kTcaRegsLast>();
     if (warp == 17) {
-      // ---------------------------------------------- the ring
+      // ---------------------------------------------- the rings
       bool ok = true;
-      int j = 0, slot = 0, ph_e = 1, step = 0, used = 0;
-      auto turn = [&]() {
-        if (++slot == kTcaSlots) {
-          slot = 0;
-          ph_e ^= 1;
-        }
-        ++used;
+      int j = 0, step = 0, used0 = 0, used1 = 0;   // entries of ring 0 and 1 so far
+      // the next slot of a ring, once it is free: 0 .. 2 * kTcaSlots - 1
+      auto next_slot = [&](int ring) {
+        const int used = ring ? used1 : used0;
+        const int slot = ring * kTcaSlots + used % kTcaSlots;
+        ok = mbar_wait_warp(eempty + 8 * slot, (used / kTcaSlots & 1) ^ 1, kSiteKvFree);
+        return slot;
       };
       TcaCursor ahead = cur;   // the lookups' cursor; cur: the copies'
       int aj = 0;
@@ -790,7 +786,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             for (int r0 = 0; r0 < kTcaGroup && ok; r0 += RE) {
               const int row0 = cur.g * kTcaGroup + r0;
               if (cur.g * kTcaGroup + (r0 & ~(kTcaRows - 1)) >= cur.s.rows) break;
-              ok = mbar_wait_warp(eempty + 8 * slot, ph_e, kSiteKvFree);
+              const int ring = r0 >= kTcaRows;   // the tile's
+              const int slot = next_slot(ring);
               if (!ok) break;
               const uint32_t dst = base + C::ORing + slot * kTcaSlot;
               if (RE % a.G == 0) {   // whole tokens: rows behind the sequence are anybody's, and dead
@@ -819,12 +816,12 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
                 cp_async_arrive(efull + 8 * slot);
               }
-              turn();
+              (ring ? used1 : used0) += 1;
             }
           }
 #pragma unroll 1
           for (int kv = 0; kv < 2 && ok; ++kv) {
-            ok = mbar_wait_warp(eempty + 8 * slot, ph_e, kSiteKvFree);
+            const int slot = next_slot(kv);
             if (!ok) break;
             const bool mine = boxes && lane >> 2 == u;
             if (kv == 0 && lane >> 2 == u)
@@ -833,7 +830,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (mine)
               tma_load_2d(base + C::ORing + slot * kTcaSlot + (lane & 3) * 16 * D, kv == 0 ? &tmK : &tmV, 0, row, efull + 8 * slot);
             if (!mine) mbar_arrive(efull + 8 * slot);
-            turn();
+            (kv ? used1 : used0) += 1;
           }
           if (++j == cur.steps()) {
             j = 0;
@@ -842,8 +839,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
       }
       // leave only once the last copies have landed, whatever became of the others
-      for (int i = max(0, used - kTcaSlots); i < used; ++i)
-        mbar_wait(efull + 8 * (i % kTcaSlots), (i / kTcaSlots) & 1, kSiteKvLoad);
+      for (int ring = 0; ring < 2; ++ring) {
+        const int used = ring ? used1 : used0;
+        for (int i = max(0, used - kTcaSlots); i < used; ++i)
+          mbar_wait(efull + 8 * (ring * kTcaSlots + i % kTcaSlots), (i / kTcaSlots) & 1, kSiteKvLoad);
+      }
     } else if ((warp == 16 || warp == 18) && elect_one()) {
       // ---------------------------------------------- tensor core, one thread a tile
       constexpr uint32_t is = umma_idesc_f16(kTcaRows, kTcaTile, false), io = umma_idesc_f16(kTcaRows, D, true);
