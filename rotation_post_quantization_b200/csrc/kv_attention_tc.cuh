@@ -350,7 +350,7 @@ struct TcaCfg {
   static constexpr int OpQ = kTcaRows * D * 2, Op = kTcaTile * D * 2;   // bytes of the fp16 operand tiles
   static constexpr int OQ = 0, OK = 2 * OpQ, OV = OK + 2 * Op, ORing = OV + kTcaVStages * Op;
   static constexpr int OMeta = ORing + 2 * kTcaSlots * kTcaSlot;        // [steps][4] scales of 16 tokens each
-  static constexpr int OCoef = OMeta + kTcaMeta * 4 * 16;               // [2][256] the rows' factors, by unit parity
+  static constexpr int OCoef = OMeta + kTcaMeta * 4 * 16;               // [2][256] the rows' factors; a tile's units take turns
   static constexpr int OBar = OCoef + 2 * kTcaGroup * 4;
   static constexpr int Bars = 21 + 2 * kTcaVStages + 4 * kTcaSlots;
   static constexpr int Smem = 1024 + OBar + 8 * Bars + 64;
@@ -435,6 +435,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const uint32_t ts = tmem + lanes + tile * 64, tp = tmem + lanes + 128 + tile * 64, to = tmem + lanes + 256 + tile * D;
     bool ok = true;
     int use = 0, step = 0, seg = 0;   // use: steps of this tile; P's place is use & 1
+    int mine = 0;                     // units of this tile
     const uint32_t pfree_t = pfree + 16 * tile;
     // PV of use u has completed (its P is free, its O is there): u the last or the one before
     auto product = [&](int u) { return mbar_wait_warp(pfree_t + 8 * (u & 1), (u >> 1) & 1, kSiteKvAccum); };
@@ -464,7 +465,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           uint32_t v[2][32];
           tmem_ld_32x32b_x32(ts, v[0]);
           tmem_ld_32x32b_x32(ts + 32, v[1]);
-          if (j == 0) coef = reinterpret_cast<const float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r];
+          if (j == 0) coef = reinterpret_cast<const float*>(smem + C::OCoef)[(mine & 1) * kTcaGroup + tile * kTcaRows + r];
           const int t = (cur.t0 + cur.z + j) * kTcaTile;
           const KvScale* meta = reinterpret_cast<const KvScale*>(smem + C::OMeta) + ((step + j) % kTcaMeta) * 4;
           const bool whole = j >= whole0 && j < whole1;
@@ -571,6 +572,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
         if (ok) ok = product(use - 1);
         if (!ok) break;
+        ++mine;
         tc_fence_after();
         const bool split = n < cur.tiles;
         float* slot = a.part + (static_cast<long long>(blockIdx.x) * 2 + (seg > 0 ? 1 : 0)) * C::SlotFloats;
@@ -627,7 +629,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     regs_give<kTcaRegsCodes>();
     const int pt = (tid - 256) & 127, half = (warp - 8) >> 2;   // half: 0 tile 0 and K, 1 tile 1 and V
     bool ok = true;
-    int seg = 0, slot = 0, ph_e = 0, ph_q = 1, stage = 0, ph_s = 1;
+    int mine = 0, slot = 0, ph_e = 0, stage = 0, ph_s = 1;   // mine: units of this half's tile
     const int stages = half ? kTcaVStages : 2;
     const uint32_t full_e = efull + 8 * kTcaSlots * half, empty_e = eempty + 8 * kTcaSlots * half;   // this half's ring
     const uint8_t* const ring = smem + C::ORing + half * kTcaSlots * kTcaSlot;
@@ -671,8 +673,10 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
       constexpr int L = D / 8, RE = kTcaSlot / (2 * D);   // pieces of a row, rows of a slot
       const int tile = half, row0 = cur.g * kTcaGroup;
       if (row0 + tile * kTcaRows < cur.s.rows) {
-        ok = mbar_wait_warp(qempty + 8 * tile, ph_q, kSiteKvFree);
-        ph_q ^= 1;
+        // The last S of the tile's unit before is there, so its first step's rows have read the
+        // factors of the one before that, and their place is free. (Counted over the tile's own
+        // units: with a unit without this tile between, nothing says that they were read.)
+        ok = mbar_wait_warp(qempty + 8 * tile, (mine & 1) ^ 1, kSiteKvFree);
 #pragma unroll 1
         for (int r0 = 0; r0 < kTcaRows; r0 += RE) {
           const uint8_t* from = take();
@@ -707,10 +711,11 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                            pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
           }
           if (c == 0)
-            reinterpret_cast<float*>(smem + C::OCoef)[(seg & 1) * kTcaGroup + tile * kTcaRows + r] =
+            reinterpret_cast<float*>(smem + C::OCoef)[(mine & 1) * kTcaGroup + tile * kTcaRows + r] =
                 __int_as_float((e - 14 + 127) << 23) * fabsf(a.scale);
           give(r0 + RE >= kTcaRows ? qfull + 8 * tile : 0u);
         }
+        ++mine;
       }
       // ---- codes
 #pragma unroll 1
@@ -726,7 +731,6 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           ph_s ^= 1;
         }
       }
-      ++seg;
       cur.next(a);
     }
   } else {
