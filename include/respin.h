@@ -362,7 +362,9 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache,
  *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * No input may overlap an output. A row that sees no token gets out 0 and lse -inf. Products are exact and
  * sums fp32; the weights are rounded to fp16 before the second product and
- * the output to bf16.
+ * the output to bf16. The value scales of the pages that a row sees may lie
+ * up to 2^64 apart (scales of 0 aside): smaller ones may count as up to 2^-64
+ * of the largest, and the tokens of pages of zeros always count in the sum.
  *
  *   q         : bf16 [N, q_heads, head_dim] (stride ld_q).
  *   q_heads   : a multiple of kv_heads, at most 1024.

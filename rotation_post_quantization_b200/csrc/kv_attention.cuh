@@ -9,7 +9,10 @@
 // and the page's scale is applied to the sum. The weights of a page carry
 // its v scale: p_j = 2^(s_j log2 e + log2 vs - M), M a running maximum of
 // that exponent, so p <= 2^15 fits fp16 and the accumulators need no scale of
-// their own; the sum l = sum p_j / vs takes them in fp32 before the rounding.
+// their own; the sum l = sum p_j ref / vs takes them in fp32 before the rounding.
+// ref is a value scale near those of the unit, so that neither the sum nor 1 / vs
+// leaves binary32 however small or large the values are: out = O / l * ref,
+// lse = M + log2 l - log2 ref (times ln 2).
 // Rounding p to fp16 is the one loss: half a step is 2^-12 of each weight
 // down to 2^-16 of the largest, and 2^-27 of the largest below (bf16 would
 // lose 2^-9), beside the 2^-9 of the bf16 output.
@@ -26,7 +29,7 @@
 // Work. The tiles of all (sequence, head, row group)s form one line that is
 // cut into equal pieces, one per block, so long and short sequences balance
 // without the host knowing a length. A piece that ends inside a line's unit
-// leaves (M, l, O) in the workspace; kv_combine_kernel joins those.
+// leaves its out and log2 of its sum in the workspace; kv_combine_kernel joins those.
 //
 // Bound: the cache's bytes. Four consumer warps and a producer warp (tensor
 // copies through a ring of kKvStages tiles of 2 * 64 * D bytes), three blocks
@@ -136,23 +139,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 struct KvScale {
   float k;        // k scale
   float lv;       // log2 of the v scale; -inf: tokens of a bad page, left out
-  float iv;       // 1 / v scale
-  float pad;
+  float iv;       // ref / v scale
+  float ref;      // the largest v scale of the unit's first looked-up pages; 1 where those are all 0
 };
 
-// A v scale of 0 goes with codes of 0, so any positive number stands for it;
-// 2^-64 keeps the page's weights in range beside pages of ordinary scales.
-__device__ __forceinline__ KvScale kv_scale_of(float ks, float vs) {
+// A v scale counts as at least 2^-64 of ref: one of 0 goes with codes of 0, so
+// any positive number stands for it, and this one keeps the page's weights in
+// range beside pages whose scales are up to 2^64 smaller than ref. (Values of a
+// smaller scale are off by less than 2^-57 ref.)
+__device__ __forceinline__ KvScale kv_scale_of(float ks, float vs, float ref) {
   KvScale s;
-  const float v = vs > 0.0f ? vs : 5.421010862427522e-20f;
+  const float v = fmaxf(vs, fmaxf(ref * 5.421010862427522e-20f, 1.17549435e-38f));
   s.k = ks;
   s.lv = __log2f(v);
-  s.iv = __fdiv_rn(1.0f, v);
-  s.pad = 0.0f;
+  s.iv = __fdiv_rn(ref, v);
+  s.ref = ref;
   return s;
 }
 
-// Partial results: [D / 4][rows] float4, then [rows] (M, l).
+// Partial results: [D / 4][rows] float4 (the piece's out), then [rows] log2 of
+// its sum of exponentials.
 __device__ __forceinline__ void kv_put_partial(float* slot, int rows, int row, int d, float4 v) {
   reinterpret_cast<float4*>(slot)[(d / 4) * rows + row] = v;
 }
@@ -200,7 +206,7 @@ struct KvAttnCfg {
   static constexpr int Join = kKvWarps * 8 * Pitch * 4 + kKvWarps * 8 * 8;
   static constexpr int Meta = kKvStages * 4 * 16;         // KvScale of each 16 tokens
   static constexpr int Smem = 1024 + kKvStages * Stage + Join + Meta + 2 * 8 * kKvStages + 64;
-  static constexpr int SlotFloats = RB * (D + 2);         // a partial result
+  static constexpr int SlotFloats = RB * (D + 1);         // a partial result
 };
 
 // tmK, tmV: uint8 [pages * H * P, D], box {D, min(P, 64)}, swizzle of D bytes.
@@ -306,20 +312,27 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       const int n = min(left, s.tiles - t);
       const int h = unit % a.c.H;
       const int batch = 32 / nsub;   // tiles whose pages a lane each looks up at once
+      float ref = 1.0f;
       for (int i0 = 0; i0 < n && ok; i0 += batch) {
         // lane: sub-box `lane` of the batch
         const int tok = (s.t0 + t + i0) * kKvTile + lane * SP;
         int row = -1;
-        KvScale sc = kv_scale_of(0.0f, 0.0f);
-        sc.lv = -INFINITY;
+        float ks = 0.0f, vs = 0.0f;
         if (tok < s.len && tok + SP > s.low && lane / nsub < n - i0) {   // (pages behind the window may be gone)
           const int page = kv_page(a.c, b, tok);
           if (page >= 0) {
             const int ph = page * a.c.H + h;
             row = ph * a.c.P + tok % a.c.P;
-            sc = kv_scale_of(a.c.k_scale[ph], a.c.v_scale[ph]);
+            ks = a.c.k_scale[ph];
+            vs = a.c.v_scale[ph];
           }
         }
+        if (i0 == 0) {
+          const float most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, vs > 0.0f ? __float_as_uint(vs) : 0u));
+          if (most > 0.0f) ref = most;
+        }
+        KvScale sc = kv_scale_of(ks, vs, ref);
+        if (row < 0) sc.lv = -INFINITY;
         for (int i = i0; i < min(n, i0 + batch) && ok; ++i) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(empty0 + 8 * stage, phase ^ 1, kSiteKvFree));
           if (!ok) break;
@@ -419,7 +432,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const int any_lo = a.window > 0 ? first_pos + row0 / Gq - a.window + 1 : 0;
 
     float acc[NT][KS][4];
-    float M[NT][2], l[NT][2];
+    float M[NT][2], l[NT][2], ref = 1.0f;
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
 #pragma unroll
@@ -432,6 +445,7 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
     for (int i = 0; i < n; ++i) {
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(full0 + 8 * stage, phase, kSiteKvLoad));
+      if (i == 0 && ok) ref = reinterpret_cast<const KvScale*>(smem + o_meta)[stage * 4].ref;
       const int tok = (s.t0 + t + i) * kKvTile + warp * 16;
       if (ok && tok <= any_hi && tok + 15 >= any_lo) {
         const KvScale sc = reinterpret_cast<const KvScale*>(smem + o_meta)[stage * 4 + warp];
@@ -589,23 +603,25 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i] = fmaf(at[i], f, o[i]);
       }
+      const float inv = ls > 0.0f ? __fdiv_rn(1.0f, ls) : 0.0f;   // a row that sees nothing is 0
+      const float L = ls == 0.0f ? -INFINITY : Mx + log2f(ls) - log2f(ref);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) o[i] = o[i] * inv * ref;
       if (split) {
 #pragma unroll
         for (int i = 0; i < D / 16; i += 4)
           kv_put_partial(slot, C::RB, 8 * x + row, d0 + i, make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
-        if (d0 == 0) reinterpret_cast<float2*>(slot + C::RB * D)[8 * x + row] = make_float2(Mx, ls);
+        if (d0 == 0) slot[C::RB * D + 8 * x + row] = L;
       } else {
-        const float inv = ls > 0.0f ? __fdiv_rn(1.0f, ls) : 0.0f;   // a row that sees nothing is 0
         const long long tokr = s.begin + gr / Gq;
         const int hq = h * Gq + gr % Gq;
         uint32_t w[D / 32];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) w[i] = pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+        for (int i = 0; i < D / 32; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
         __nv_bfloat16* to = a.out + tokr * a.ldo + static_cast<long long>(hq) * D + d0;
         if constexpr (D == 128) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
         else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-        if (a.lse != nullptr && d0 == 0)
-          a.lse[tokr * a.Hq + hq] = ls == 0.0f ? -INFINITY : (Mx + log2f(ls)) * 0.693147180559945f;
+        if (a.lse != nullptr && d0 == 0) a.lse[tokr * a.Hq + hq] = L * 0.693147180559945f;
       }
     }
     ++seg;
@@ -661,7 +677,7 @@ __global__ void __launch_bounds__(kKvJoinThreads) kv_combine_kernel(const KvAttn
     }
   }
   // their results: of piece c - 1 its last segment (the second slot unless it begins with the unit), of the others the first
-  const long long slot = static_cast<long long>(RB) * (D + 2);
+  const long long slot = static_cast<long long>(RB) * (D + 1);
   const float* first = j.part + (2LL * (c - 1) + (f0 == u0 ? 0 : 1)) * slot;
   const float* rest = j.part + 2LL * c * slot;
   // Few pieces: a thread for each (row, 4 dims). Many (a long context over many blocks): a warp takes 32
@@ -676,7 +692,7 @@ __global__ void __launch_bounds__(kKvJoinThreads) kv_combine_kernel(const KvAttn
     const int row = at % RB, d0 = at / RB * 4;
     const bool live = at < RB * (D / 4) && row < rows;
     float M = -INFINITY, l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto add = [&](float m2, float l2, const float4& x) {
+    auto add = [&](float m2, float l2, const float4& x) {   // l2 times 2^m2 of weight, x the weighted sum
       const float Mn = fmaxf(M, m2);
       const float f = M == -INFINITY ? 0.0f : ex2(M - Mn), g = m2 == -INFINITY ? 0.0f : ex2(m2 - Mn);
       M = Mn;
@@ -690,8 +706,7 @@ __global__ void __launch_bounds__(kKvJoinThreads) kv_combine_kernel(const KvAttn
 #pragma unroll 4
       for (int i = i0p; i < pieces; i += di) {
         const float* p = i == 0 ? first : rest + 2LL * (i - 1) * slot;
-        const float2 ml = reinterpret_cast<const float2*>(p + RB * D)[row];
-        add(ml.x, ml.y, reinterpret_cast<const float4*>(p)[at]);
+        add(p[RB * D + row], 1.0f, reinterpret_cast<const float4*>(p)[at]);
       }
     }
     if (wide) {   // the same for the whole block

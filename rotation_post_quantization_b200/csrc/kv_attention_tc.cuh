@@ -355,7 +355,7 @@ struct TcaCfg {
   static constexpr int Bars = 21 + 2 * kTcaVStages + 4 * kTcaSlots;
   static constexpr int Smem = 1024 + OBar + 8 * Bars + 64;
   static constexpr int Columns = 512;
-  static constexpr int SlotFloats = kTcaGroup * (D + 2);
+  static constexpr int SlotFloats = kTcaGroup * (D + 1);
 };
 
 // tmQ: bf16 [N][Hq][D], box {D, G, rows of a slot / G} (not used where G does not divide those rows);
@@ -454,7 +454,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int first_t = (cur.t0 + cur.z) * kTcaTile;
         const int whole0 = (max(0, __reduce_max_sync(0xFFFFFFFFu, lo) - first_t) + kTcaTile - 1) / kTcaTile;
         const int whole1 = (__reduce_min_sync(0xFFFFFFFFu, hi) + 1 - first_t) / kTcaTile;   // (below 0: none)
-        float M = -INFINITY, l = 0.0f, coef = 0.0f;
+        float M = -INFINITY, l = 0.0f, coef = 0.0f, ref = 1.0f;
         bool there = false;   // S of the step has been seen complete
         for (int j = 0; j < n; ++j, ++use) {
           // S of this step also says that P's place is free: its arrival follows every product that
@@ -468,6 +468,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           if (j == 0) coef = reinterpret_cast<const float*>(smem + C::OCoef)[(mine & 1) * kTcaGroup + tile * kTcaRows + r];
           const int t = (cur.t0 + cur.z + j) * kTcaTile;
           const KvScale* meta = reinterpret_cast<const KvScale*>(smem + C::OMeta) + ((step + j) % kTcaMeta) * 4;
+          if (j == 0) ref = meta->ref;
           const bool whole = j >= whole0 && j < whole1;
           const bool unseen = M == -INFINITY && t <= hi && t + kTcaTile - 1 >= lo;   // the row's first tokens
           // a factor of 0 (all products are 0, or are to count as 0) becomes one that keeps -inf
@@ -576,7 +577,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_after();
         const bool split = n < cur.tiles;
         float* slot = a.part + (static_cast<long long>(blockIdx.x) * 2 + (seg > 0 ? 1 : 0)) * C::SlotFloats;
-        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;
+        const float inv = l > 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;   // a row that sees nothing is 0
+        const float L = l == 0.0f ? -INFINITY : M + log2f(l) - log2f(ref);
         __nv_bfloat16* op = a.out + (cur.s.begin + tok) * a.ldo + static_cast<long long>(hq) * D;
         const bool wide = (reinterpret_cast<uintptr_t>(a.out) | (a.ldo * 2)) % 32 == 0;
 #pragma unroll 1
@@ -587,6 +589,8 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
           tmem_wait_ld();
           tmem_values(v);
           if (!live) continue;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv * ref);
           if (split) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -599,7 +603,7 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
               uint32_t w[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                w[k] = pack_bf16x2(__uint_as_float(v[i + 2 * k]) * inv, __uint_as_float(v[i + 2 * k + 1]) * inv);
+                w[k] = pack_bf16x2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1]));
               uint32_t* at = reinterpret_cast<uint32_t*>(op + 32 * c + i);
               if (wide) {
                 st_global_v8(at, w);
@@ -614,10 +618,9 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_before();
         if (live) {
           if (split)
-            reinterpret_cast<float2*>(slot + kTcaGroup * D)[row - row0] = make_float2(M, l);
+            slot[kTcaGroup * D + row - row0] = L;
           else if (a.lse != nullptr)
-            a.lse[(cur.s.begin + tok) * static_cast<long long>(a.Hq) + hq] =
-                l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945f;
+            a.lse[(cur.s.begin + tok) * static_cast<long long>(a.Hq) + hq] = L * 0.693147180559945f;
         }
       }
       step += n;
@@ -747,21 +750,25 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         return slot;
       };
       TcaCursor ahead = cur;   // the lookups' cursor; cur: the copies'
-      int aj = 0;
+      int aj = 0, au = 0;        // its step of the unit, its unit
+      int ref_u = -1;            // the unit that the last lookups ended in, and its ref
+      float ref_last = 1.0f;
       while (cur.left > 0 && ok) {
         // ---- page ids and scales of eight steps: lane / 4, 16 tokens a lane
-        int b = -1, h = 0, t = 0;
+        int b = -1, h = 0, t = 0, unit = -1;
 #pragma unroll 1
         for (int u = 0; u < 8 && ahead.left > 0; ++u) {
           if (lane >> 2 == u) {
             b = ahead.b;
             h = ahead.h;
+            unit = au;
             t = (ahead.t0 + ahead.z + aj) * kTcaTile + 16 * (lane & 3);
             const int SP = min(a.c.P, kTcaTile);
             if (t >= ahead.s.len || (t & ~(SP - 1)) + SP <= ahead.low) b = -1;   // (pages behind the window may be gone)
           }
           if (++aj == ahead.steps()) {
             aj = 0;
+            ++au;
             ahead.next(a);
           }
         }
@@ -776,7 +783,20 @@ kv_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             vs = a.c.v_scale[phd];
           }
         }
-        KvScale sc = kv_scale_of(ks, vs);
+        // a unit's ref, from the lookups it begins in
+        float most = vs > 0.0f ? vs : 0.0f, ref = 0.0f;
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u) {
+          const float m = __shfl_sync(0xFFFFFFFFu, most, 4 * u);
+          if (__shfl_sync(0xFFFFFFFFu, unit, 4 * u) == unit) ref = fmaxf(ref, m);
+        }
+        if (unit == ref_u) ref = ref_last;
+        else if (ref == 0.0f) ref = 1.0f;
+        ref_u = __shfl_sync(0xFFFFFFFFu, unit, 31);
+        ref_last = __shfl_sync(0xFFFFFFFFu, ref, 31);
+        KvScale sc = kv_scale_of(ks, vs, ref);
         if (row < 0) sc.lv = -INFINITY;
         // a page's first 16 tokens name its copy; tokens of no page keep what the slot holds (finite codes)
         const int SP = min(a.c.P, kTcaTile);   // rows of a copy
