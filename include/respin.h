@@ -361,8 +361,8 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache,
  *           and j <= p (causal)  and j > p - window (window > 0)
  *     out = sum_j softmax(s)_j v_j,   lse = log sum_j exp(s_j)
  * No input may overlap an output. A row that sees no token gets out 0 and lse -inf. Products are exact and
- * sums fp32; the weights are rounded to fp16 before the second product and
- * the output to bf16. The value scales of the pages that a row sees may lie
+ * sums fp32; the weights are rounded to fp16 before the second product (2^-11
+ * of each, those far below the largest 2^-31 of it) and the output to bf16. The value scales of the pages that a row sees may lie
  * up to 2^64 apart (scales of 0 aside): smaller ones may count as up to 2^-64
  * of the largest, and the tokens of pages of zeros always count in the sum.
  *

@@ -4,8 +4,8 @@
 //   s_j = (q . k_j) * scale,  out = sum_j softmax(s)_j v_j,  lse = log sum_j e^(s_j)
 //
 // Numbers. Codes are whole numbers up to 127 and exact in fp16; so are a row
-// of q scaled by a power of two (amax to [2^14, 2^15)) down to 2^-38 of its
-// amax. The products of the tensor cores are then exact and summed in fp32,
+// of q scaled by a power of two (amax to [2^14, 2^15)) down to 2^-31 of its
+// amax; smaller values of q are off by 2^-39 of it at most. The products of the tensor cores are then exact and summed in fp32,
 // and the page's scale is applied to the sum. The weights of a page carry
 // its v scale: p_j = 2^(s_j log2 e + log2 vs - M), M a running maximum of
 // that exponent, so p <= 2^15 fits fp16 and the accumulators need no scale of
@@ -13,9 +13,11 @@
 // ref is a value scale near those of the unit, so that neither the sum nor 1 / vs
 // leaves binary32 however small or large the values are: out = O / l * ref,
 // lse = M + log2 l - log2 ref (times ln 2).
-// Rounding p to fp16 is the one loss: half a step is 2^-12 of each weight
-// down to 2^-16 of the largest, and 2^-27 of the largest below (bf16 would
-// lose 2^-9), beside the 2^-9 of the bf16 output.
+// Rounding p to fp16 is the one loss: half a step is 2^-11 of each weight
+// down to 2^-20 of the largest, and 2^-31 of the largest below (bf16 would
+// lose 2^-8), beside the 2^-8 of the bf16 output. (The largest is 2^6 at least.
+// With 2^2 and a lag of 2^13 weights below 2^-27 of it were lost; wide logits
+// rescale more often now, see kv_attention_tc.cuh, decode takes the same time.)
 //
 // Layout. A warp takes 16 tokens of a 64-token tile and 8 rows at a time with
 // the transposed products S^T = K Q^T and O^T = V^T P^T: with at most 8 rows
@@ -56,8 +58,8 @@ constexpr int kKvMaxBlocks = 592;    // 4 per SM
 constexpr int kKvMinTiles = 4;       // least piece of a block
 constexpr int kKvFewRows = 16;       // rows a key head up to which a sequence is this kernel's
 constexpr int kKvPlan = 3;           // int4s a block leaves about its piece (KvJoin)
-constexpr float kKvBias = 2.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^15 in fp16
-constexpr float kKvLazy = 13.0f;     // the running maximum may lag by 2^13
+constexpr float kKvBias = 6.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^15 in fp16
+constexpr float kKvLazy = 9.0f;      // the running maximum may lag by 2^9
 
 struct KvAttnArgs {
   KvView c;
