@@ -367,7 +367,9 @@ respin_status_t respin_kv_read(const respin_kv_cache_t* cache,
  * of the largest, and the tokens of pages of zeros always count in the sum.
  *
  *   q         : bf16 [N, q_heads, head_dim] (stride ld_q).
- *   q_heads   : a multiple of kv_heads, at most 1024.
+ *   q_heads   : a multiple of kv_heads, at most 1024. With R = N * q_heads /
+ *               kv_heads, R < 2^31 and kv_heads * (B + R / 256) *
+ *               (max_pages * page_size + 448) / 64 <= 2^38 (else UNSUPPORTED).
  *   max_q     : at least the most rows of a sequence, 0 if unknown (a value
  *               below the truth may leave longer sequences out: 512). Without
  *               cu it is N / B, whatever is given.

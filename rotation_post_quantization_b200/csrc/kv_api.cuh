@@ -318,6 +318,13 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
   if (static_cast<long long>(batch->N) * (q_heads / H) > 0x7FFFFFFFLL)
     return fail(RESPIN_ERR_UNSUPPORTED, "N * q_heads / kv_heads = %lld rows: at most 2^31 - 1",
                 static_cast<long long>(batch->N) * (q_heads / H));
+  // Tiles of 64 tokens (a unit's fixed cost aside) in both kernels' lines of work at most: a sequence has
+  // one row group of few rows, or one for each 256 rows and a part. A block's piece is counted in 32 bits;
+  // both kernels have 128 blocks at least.
+  const long long line = H * (batch->B + static_cast<long long>(batch->N) * (q_heads / H) / kTcaGroup) *
+                         (static_cast<long long>(batch->max_pages) * cache->page_size / kKvTile + 1 + kTcaUnitCost);
+  if (line > 1LL << 38)
+    return fail(RESPIN_ERR_UNSUPPORTED, "kv_heads * (B + rows / 256) * max_pages * page_size / 64 = %lld: at most 2^38", line);
   if (batch->cu == nullptr) max_q = batch->N / batch->B;   // what it is, whatever was given
   if (q == nullptr || out == nullptr || workspace == nullptr)
     return fail(RESPIN_ERR_INVALID_ARG, "q, out and workspace must be non-NULL");

@@ -279,11 +279,10 @@ kv_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
       }
     }
     if (lane == 0) {
-      const long long cap = left > 0 ? left : 0;   // < 2^31: checked by the host
+      const long long cap = left > 0 ? left : 0;   // < 2^31: the host bounds the line
       sh[0] = b_at;
       *reinterpret_cast<volatile long long*>(sh + 4) = off;
       sh[2] = static_cast<int>(cap);
-      sh[3] = static_cast<int>(chunk);
       const long long from = min(p0, total);
       int4 pl = make_int4(-1, 0, 0, 0), pm = make_int4(1, static_cast<int>(from & 0xFFFFFFFF), static_cast<int>(from >> 32), 0);
       if (cap > 0) {   // where the piece begins: sequence, row, head, tiles of the unit before it; its tiles
