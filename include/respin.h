@@ -312,7 +312,9 @@ typedef struct {
  * that does not fit (negative, decreasing, beyond N or the table) or a page id
  * outside the cache is recorded (respin_device_status: 512, 511) and its
  * tokens are left out; nothing outside the given buffers is touched. The
- * length of a sequence without rows is not looked at.
+ * length of a sequence without rows is not looked at. More rows than the
+ * sequence has tokens: append leaves the sequence out (512), read the rows
+ * before its first token (512), attention takes those as rows that see nothing.
  */
 typedef struct {
   const int32_t* cu;           /* [B + 1], or NULL: N / B rows each */

@@ -399,7 +399,7 @@ respin_status_t respin_kv_attention(const respin_kv_cache_t* cache, const respin
     e = launch_dependent3(v.fn, dim3(static_cast<unsigned>(few.blocks), 1, 1), v.threads, v.smem, s, args);
     if (e != cudaSuccess) return cuda_fail(e, "kv_attn_kernel launch");
   }
-  few.parts = few.rows * D / 4 / 64;   // 2 or 4 at head_dim 128
+  few.parts = few.rows * D / 4 / 64;   // 4 or 8 at head_dim 128, 2 or 4 at 64
   many.parts = D / 8;
   const int joins = (few.blocks > 0 ? (few.blocks - 1) * few.parts : 0) + (many.blocks > 0 ? (many.blocks - 1) * many.parts : 0);
   if (joins > 0) {

@@ -37,7 +37,7 @@
 // copies through a ring of kKvStages tiles of 2 * 64 * D bytes), three blocks
 // an SM (two with four stages: 75 us where three take 66). 64 sequences of 32
 // query heads over 8 at 4096 tokens: 97 us, 5.5 TB/s with the join; two of 64
-// over 8 at 131071: 90 us, 5.9 TB/s, and 9 us for the join of 28 pieces a unit.
+// over 8 at 131071: 92 us, 5.8 TB/s, and 11 us for the join of 28 pieces a unit.
 #pragma once
 
 #include <cuda.h>
@@ -56,7 +56,10 @@ constexpr int kKvWarps = 4;          // consumer warps, 16 tokens each
 constexpr int kKvThreads = (kKvWarps + 1) * 32;
 constexpr int kKvMaxBlocks = 592;    // 4 per SM
 constexpr int kKvMinTiles = 4;       // least piece of a block
-constexpr int kKvFewRows = 16;       // rows a key head up to which a sequence is this kernel's
+// Rows a key head up to which a sequence is this kernel's: what it is built for. kv_attention_tc.cuh takes
+// longer at 16 rows and below: 64 sequences at 4096 tokens, 8 key heads of 128, 16 rows 240 us (here 170),
+// 12 rows 154 (107), 8 rows 236 (86); heads of 64 215 (78); one sequence of 200 tokens 24.6 (18.0).
+constexpr int kKvFewRows = 16;
 constexpr int kKvPlan = 3;           // int4s a block leaves about its piece (KvJoin)
 constexpr float kKvBias = 6.0f;      // p <= 2^(kKvBias + kKvLazy) = 2^15 in fp16
 constexpr float kKvLazy = 9.0f;      // the running maximum may lag by 2^9

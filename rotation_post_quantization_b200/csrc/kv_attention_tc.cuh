@@ -46,10 +46,10 @@
 // Two 4096-token prompts, 32 query heads over 8: 380 us, 723 TFLOP/s; one of
 // 8192: 675 us, 814 TFLOP/s. Logits of a standard deviation of 8 (natural units)
 // move the maximum often enough to take 31 % longer (498 us; 454 with a lag of
-// 2^13, which loses the weights below 2^-27 of the largest).
+// 2^13 in place of 2^9, which loses the weights below 2^-27 of the largest).
 //
 // Tensor memory: S0, S1 (64 columns each), P0, P1 (2 x 32 each), O0, O1 (D
-// each). Shared memory at D = 128: Q 64 KB, K 32 KB, V 48 KB, ring 64 KB.
+// each). Shared memory at D = 128: Q 64 KB, K 32 KB, V 48 KB, rings 64 KB.
 //
 // Work: as in kv_attention.cuh one line of steps cut into equal pieces, here
 // with each row group's own number of steps (causal rows see fewer).
@@ -70,8 +70,11 @@ constexpr int kTcaVStages = 3;
 constexpr int kTcaMinTiles = 8;     // least piece of a block
 // A unit's queries, first step and output cost about as much as six steps;
 // the line of work counts them, so that blocks of many short units (a causal
-// prompt's first rows) get fewer of their steps. Two 4096-token prompts, at a
-// cost of 3, 5, 6, 7, 10: 428, 387, 380, 384, 394 us.
+// prompt's first rows) get fewer of their steps. Two 4096-token prompts of
+// heads of 128, at a cost of 3, 4, 6, 8, 10: 453, 414, 379, 385, 391 us; 64 of
+// 512 tokens: 295, 277, 272, 279, 283. Heads of 64 would have 4: 324, 326, 332,
+// 340, 346 us and 209, 209, 217, 223, 225; chunks of 511 rows behind 8000 tokens
+// with a window of 1000 are within 3 % of one another.
 constexpr int kTcaUnitCost = 6;
 static_assert(kTcaMinTiles > kTcaUnitCost, "a piece has a step");
 constexpr int kTcaMaxBlocks = 160;  // one per SM

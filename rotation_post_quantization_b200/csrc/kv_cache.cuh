@@ -17,8 +17,9 @@
 // call finds s = s_old and writes the same bytes again.
 //
 // Both directions are memory bound (3 bytes an element). Measured: 6906 tokens
-// of 32 heads of 128 into pages of 16, 42 us (4.0 TB/s); 22006 tokens of 8
-// heads read back, 27.5 us (5.2 TB/s).
+// of 32 heads of 128 into pages of 16, 42 us (4.0 TB/s; a warp has no load on its
+// way while it forms a unit's codes); 22006 tokens of 8
+// heads read back, 28 us (5.1 TB/s).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -10,7 +10,10 @@
 // keeps 2^-32 there; in fp32 it would be off by up to 2^-4) and reduced by
 // whole turns before the fp32 sine and cosine.
 //
-// Memory bound: every element is read and written once (4 bytes an element).
+// Every element is read and written once (4 bytes an element), which would take
+// 13 us for 4096 tokens of 40 heads. What it takes beyond that: a block loads no
+// vector before its angles are formed, with all blocks in one wave, and the
+// warps then issue in 66 % of the cycles.
 // A vector of d values is held by d/8 neighbouring lanes, both values of a
 // pair in the same one (two runs of 8 bytes a lane, half the rotated width
 // apart), so only the sum of squares needs shuffles. A block takes several
